@@ -65,7 +65,8 @@ typedef enum {
   JOLT_ERR_BAD_BLOB = 9            /* blob header failed validation */
 } jolt_status;
 
-typedef enum { JOLT_BF16 = 0, JOLT_F32 = 1 } jolt_dtype;
+/* JOLT_F16 is a type of the paged cache's rows, queries and outputs only */
+typedef enum { JOLT_BF16 = 0, JOLT_F32 = 1, JOLT_F16 = 2 } jolt_dtype;
 typedef enum { JOLT_EXACT = 0, JOLT_RANDOMIZED = 1 } jolt_method;
 
 /* Shape of ONE of the two cache tensors K and V, both [n_layers, n_heads, n_tokens, head_dim],
@@ -244,6 +245,13 @@ jolt_status jolt_attend_scratch_size(const jolt_shape* shape, int32_t max_token_
 jolt_status jolt_attend(const void* blob_dev, const void* ws_dev, size_t ws_bytes, int32_t layer, const float* q_dev,
                         int32_t n_q_heads, float* out_dev, void* scratch_dev, size_t scratch_bytes, void* stream);
 
+/* jolt_attend that also gives the softmax's log-sum-exp, lse_dev [n_q_heads] fp32 (natural
+ * logarithm of sum_t exp(s_t)): with it, attention over further keys can be joined to the
+ * output (the prefix of jolt_cache_attend).  Same arguments and outputs otherwise. */
+jolt_status jolt_attend_state(const void* blob_dev, const void* ws_dev, size_t ws_bytes, int32_t layer,
+                              const float* q_dev, int32_t n_q_heads, float* out_dev, float* lse_dev,
+                              void* scratch_dev, size_t scratch_bytes, void* stream);
+
 /* Per-block b-bit quantisation of the caches themselves, without factors or rotation: the
  * plain quantisation baseline of the introduction of "A JoLT for the KV Cache ... Joint Tucker
  * and JL-Residual Allocation for LLMs" (JoLT's error is roughly an order of magnitude below it
@@ -258,6 +266,113 @@ jolt_status jolt_attend(const void* blob_dev, const void* ws_dev, size_t ws_byte
 jolt_status jolt_quant_baseline(const jolt_shape* shape, const void* k_dev, const void* v_dev, int32_t bits,
                                 void* codes_dev, void* scales_dev, double* sq_dev, void* ws_dev, size_t ws_bytes,
                                 void* stream);
+
+/* ---- paged cache of block-quantised rows --------------------------------------------------
+ * The cache of what is not a factored prompt: the rows generated after a compressed prompt, or
+ * whole sequences.  Rows arrive one, a few or a chunk at a time, are stored by the residual
+ * quantiser (16 consecutive features per block, fp16 lo = round-down(min), step =
+ * round-up((max - lo)/(2^b - 1)), code = round-half-even((x - lo)/step)) and are attended over
+ * in place (no counterpart on the pages, which compress a finished prompt only).
+ *
+ * One jolt_cache is one layer's pool of pages; K and V have their own bit-widths.  Layout of
+ * the codes: [n_pages][n_heads][page_size][head_dim * bits / 8] bytes, the codes of a row as one
+ * little-endian bit string (2 * bits bytes per block); of the scales:
+ * [n_pages][n_heads][page_size][head_dim / 16] fp16 pairs (lo, step).  Pointers 16-byte aligned.
+ *   head_dim 64 or 128; page_size a power of two in [16, 4096]; bits 2, 4 or 8. */
+typedef struct {
+  int32_t n_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t n_pages;
+  int32_t bits_k;
+  int32_t bits_v;
+  void* k_codes_dev;
+  void* k_scales_dev;
+  void* v_codes_dev;
+  void* v_scales_dev;
+} jolt_cache;
+
+/* A ragged batch: the rows that a call writes, reads or queries are the last ones of each
+ * sequence.  Row starts[b] + i (0 <= i < n_b = starts[b + 1] - starts[b]) stands at position
+ * lens[b] - n_b + i of sequence b; position t is slot t % page_size of page
+ * page_table[b][t / page_size].  All arrays are device memory and are read when the kernels run:
+ * a captured graph replays with whatever they then hold.
+ *   n_seqs    : sequences (0 is allowed: nothing is done)
+ *   max_pages : row pitch of page_table (entries behind a sequence's last page are not read)
+ *   max_new   : the most rows of one sequence (an upper bound; jolt_cache_attend chooses its kernel by it)
+ *   n_rows    : rows of the dense tensors; rows at or behind starts[n_seqs] are left as they were
+ *   status_dev: one uint32 of device memory, OR-ed with what the kernels find (never cleared by
+ *               them); jolt_cache_check reads it
+ * A sequence with n_b < 0, n_b > max_new, rows outside [0, n_rows), lens[b] < n_b or
+ * lens[b] > max_pages * page_size is left out and a page index outside [0, n_pages) makes its rows
+ * unwritten, read as zeros or unseen; both set JOLT_ERR_INVALID_ARG's bit in the status word.  With
+ * starts that do not ascend, rows of other sequences may be left out too. */
+typedef struct {
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t max_new;
+  int32_t n_rows;
+  const int32_t* page_table_dev; /* [n_seqs][max_pages] */
+  const int32_t* lens_dev;       /* [n_seqs], new rows included */
+  const int32_t* starts_dev;     /* [n_seqs + 1] */
+  uint32_t* status_dev;
+} jolt_cache_batch;
+
+/* Quantise new rows into their pages.  k_dev, v_dev: [n_rows][n_heads][head_dim] of `dtype` (any
+ * jolt_dtype), with strides (in elements) between rows and heads; features are contiguous.
+ * Values beyond +-65504 (infinities too) are stored as +-65504 and NaN as 0; both set
+ * JOLT_ERR_NUMERIC's bit in the status word.  No page may be written through two sequences of
+ * one call or by two calls at once (a row would mix both).  Asynchronous. */
+jolt_status jolt_cache_write(const jolt_cache* cache, const jolt_cache_batch* batch, const void* k_dev,
+                             const void* v_dev, int32_t dtype, int64_t k_row_stride, int64_t k_head_stride,
+                             int64_t v_row_stride, int64_t v_head_stride, void* stream);
+
+/* Read stored rows back: k_out_dev, v_out_dev [n_rows][n_heads][head_dim] of `dtype` with strides
+ * as in jolt_cache_write; x = lo + code * step in fp32, rounded once.  (A whole sequence is read
+ * with n_b = lens[b].)  Asynchronous. */
+jolt_status jolt_cache_read(const jolt_cache* cache, const jolt_cache_batch* batch, int32_t dtype, void* k_out_dev,
+                            void* v_out_dev, int64_t k_row_stride, int64_t k_head_stride, int64_t v_row_stride,
+                            int64_t v_head_stride, void* stream);
+
+/* What jolt_cache_attend computes beside plain attention. */
+typedef struct {
+  float scale;          /* of q . k; 0 = 1 / sqrt(head_dim) */
+  float softcap;        /* c > 0: s = c tanh(s / c), before the bias; 0 = none */
+  int32_t window;       /* w > 0: a row at position p sees keys at positions above p - w only; 0 = all */
+  int32_t mask_words;   /* 32-bit words per row of `mask`, at least max_new / 32 */
+  const float* slopes_dev;       /* [n_q_heads]: s -= slope * (p_query - p_key); NULL = no bias */
+  const int32_t* positions_dev;  /* [n_rows] positions of the new rows, as queries and as keys; NULL =
+                                    their place in the sequence.  Below lens[b] - n_b is not allowed */
+  const uint32_t* mask_dev;      /* [n_rows][mask_words]: bit j of row i is set if row i sees new row j
+                                    of its sequence (a tree: itself and its ancestors); NULL = causal */
+  const float* prefix_out_dev;   /* [n_rows][n_q_heads][head_dim] fp32 and */
+  const float* prefix_lse_dev;   /* [n_rows][n_q_heads] fp32: attention of the same queries over other
+                                    keys (jolt_attend_state), joined to the output; both or neither */
+} jolt_cache_attend_options;
+
+/* Attention of the batch's rows over their sequences' pages.  The rows' own keys and values are
+ * already written (they are the last n_b of lens[b]).  A row sees the keys before the new rows and
+ * those new rows that its mask allows, both inside the window; query head j reads KV head
+ * j / (n_q_heads / n_heads).  o = sum_t p_t v_t with p the softmax of s; a row that sees nothing
+ * gives its prefix, or zeros.  The stored values enter the products as fp16 (one rounding of
+ * lo + code * step), the weights p too; sums, maxima and the softmax are fp32.
+ *   q_dev   : [n_rows][n_q_heads][head_dim] of `dtype` (JOLT_BF16 or JOLT_F16), strides in elements
+ *   out_dev : the same shape and type, its own strides
+ *   scratch_dev: jolt_cache_attend_scratch_size bytes, 256-byte aligned, contents irrelevant; two
+ *     calls (or replayed graphs) that may run at once need one each
+ * Results do not depend on the other sequences of the batch beyond the order of fp32 sums, and are
+ * the same in every run of the same call.  Asynchronous. */
+jolt_status jolt_cache_attend_scratch_size(const jolt_cache* cache, const jolt_cache_batch* batch, int32_t n_q_heads,
+                                           size_t* bytes);
+jolt_status jolt_cache_attend(const jolt_cache* cache, const jolt_cache_batch* batch,
+                              const jolt_cache_attend_options* opts, const void* q_dev, int32_t dtype,
+                              int32_t n_q_heads, int64_t q_row_stride, int64_t q_head_stride, void* out_dev,
+                              int64_t out_row_stride, int64_t out_head_stride, void* scratch_dev,
+                              size_t scratch_bytes, void* stream);
+
+/* Read a batch's status word (SYNCHRONISES the stream): JOLT_OK, or the error that the kernels
+ * recorded (INVALID_ARG, NUMERIC, TIMEOUT).  The word is not cleared. */
+jolt_status jolt_cache_check(const uint32_t* status_dev, void* stream);
 
 /* Per-unit sums of squares (the introduction reports the relative Frobenius error of K and
  * of V separately): sq_dev[2*u] = ||X_u||^2, sq_dev[2*u+1] = ||X_u - Y_u||^2

@@ -8,37 +8,63 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
+OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libjolt.so")
-SOURCES = ["jolt_api.cu"]
+SOURCES = ["jolt_api.cu", "cache_api.cu"]
 DEPS = ["jolt_api.cu", "common.cuh", "gemm.cuh", "kernels.cuh", "misc.cuh", "umma.cuh", "eig_cluster.cuh", "chol.cuh",
-        "fp16_exact.cuh", "table_tc.cuh", "attend.cuh", "eig_large.cuh"]
+        "fp16_exact.cuh", "table_tc.cuh", "attend.cuh", "eig_large.cuh", "host.cuh", "cache_api.cu", "cache.cuh", "cache_attend.cuh"]
+# the headers each cache source reaches; every other source is rebuilt when anything but these changes
+CACHE = {"cache_api.cu", "cache.cuh", "cache_attend.cuh"}
 
 
-def nvcc_cmd(out: str = LIB, extra=()) -> list:
+def nvcc_cmd(source: str, out: str, extra=()) -> list:
     return (["nvcc", "-std=c++17", "-O3", "-lineinfo",
              "-gencode", "arch=compute_100a,code=sm_100a",
-             "-Xcompiler", "-fPIC", "-shared",
+             "-Xcompiler", "-fPIC", "-c",
              "-I", os.path.join(ROOT, "include"),
-             "-o", out] + [os.path.join(CSRC, s) for s in SOURCES] + list(extra) + ["-lcusolver"])
+             "-o", out, os.path.join(CSRC, source)] + list(extra))
+
+
+def link_cmd(objects: list, out: str) -> list:
+    return (["nvcc", "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", out] + objects + ["-lcusolver"])
+
+
+def _newer(target: str, paths) -> bool:
+    """Whether target exists and is no older than any of paths."""
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in paths)
+
+
+def _inputs(source: str) -> list:
+    """Files whose change rebuilds a source's object."""
+    deps = DEPS if source in CACHE else [d for d in DEPS if d not in CACHE]
+    return [os.path.join(CSRC, d) for d in deps] + [os.path.join(ROOT, "include", "jolt.h")]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    srcs = [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", "jolt.h")]
-    return all(os.path.getmtime(s) <= t for s in srcs)
+    return _newer(LIB, [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", "jolt.h")])
 
 
 def build(force: bool = False, verbose: bool = True) -> str:
+    """Compile the sources that changed (side by side) and link the library."""
     if not force and up_to_date():
         return LIB
-    cmd = nvcc_cmd()
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
+    os.makedirs(OBJ, exist_ok=True)
+    running, objects = [], []
+    for source in SOURCES:
+        obj = os.path.join(OBJ, source.replace(".cu", ".o"))
+        objects.append(obj)
+        if not force and _newer(obj, _inputs(source)):
+            continue
+        cmd = nvcc_cmd(source, obj + ".tmp")
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        running.append((obj, cmd, subprocess.Popen(cmd)))
+    for obj, cmd, p in running:
+        if p.wait() != 0:
+            raise subprocess.CalledProcessError(p.returncode, cmd)
+        os.replace(obj + ".tmp", obj)
     tmp = LIB + ".tmp"
-    cmd[cmd.index("-o") + 1] = tmp
-    subprocess.run(cmd, check=True)
+    subprocess.run(link_cmd(objects, tmp), check=True)
     os.replace(tmp, LIB)
     return LIB
 

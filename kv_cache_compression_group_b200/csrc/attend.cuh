@@ -55,6 +55,7 @@ struct AttendArgs {
   float* part;            // [H][nch][G][2 + rTmax + D] scratch: chunk records
   int nch;                // token chunks per KV head
   float* out;             // [nq][D]
+  float* lse;             // [nq] log-sum-exp of the scores, or null
 };
 
 __device__ __forceinline__ const UnitHeader& att_unit(const unsigned char* blob, int u) {
@@ -322,6 +323,7 @@ __global__ void __launch_bounds__(att::THREADS) attend_combine_kernel(AttendArgs
     }
     stat[0] = M;
     stat[1] = 1.f / E;
+    if (A.lse) A.lse[j] = M + logf(E);
   }
   __syncthreads();
   const float inv = stat[1];

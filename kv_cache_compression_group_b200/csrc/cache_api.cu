@@ -1,0 +1,212 @@
+// Host side of the paged cache's C ABI: argument checks and launches.
+#include <cmath>
+
+#include "jolt.h"
+#include "common.cuh"
+#include "host.cuh"
+#include "cache.cuh"
+#include "cache_attend.cuh"
+
+using namespace jolt;
+
+namespace {
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+jolt_status cache_args(const jolt_cache* c, const jolt_cache_batch* b, CacheArgs* ca, BatchArgs* ba) {
+  if (!c || !b) return fail(JOLT_ERR_INVALID_ARG, "null cache or batch");
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "cache head_dim %d not in {64, 128}", c->head_dim);
+  if (c->n_heads < 1 || c->n_heads > 65535) return fail(JOLT_ERR_INVALID_ARG, "n_heads %d", c->n_heads);
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)))
+    return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "page_size %d is not a power of two in [16, 4096]", c->page_size);
+  if (c->n_pages < 1) return fail(JOLT_ERR_INVALID_ARG, "n_pages %d", c->n_pages);
+  for (int bits : {c->bits_k, c->bits_v})
+    if (bits != 2 && bits != 4 && bits != 8)
+      return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "cache bits %d not in {2, 4, 8}", bits);
+  if (!c->k_codes_dev || !c->k_scales_dev || !c->v_codes_dev || !c->v_scales_dev)
+    return fail(JOLT_ERR_INVALID_ARG, "null cache pool");
+  if (!aligned16(c->k_codes_dev) || !aligned16(c->k_scales_dev) || !aligned16(c->v_codes_dev) ||
+      !aligned16(c->v_scales_dev))
+    return fail(JOLT_ERR_INVALID_ARG, "cache pools must be 16-byte aligned");
+  if (b->n_seqs < 0 || b->max_pages < 0 || b->max_new < 0 || b->n_rows < 0)
+    return fail(JOLT_ERR_INVALID_ARG, "negative batch size");
+  if (b->n_seqs > 0 && (!b->page_table_dev || !b->lens_dev || !b->starts_dev || !b->status_dev))
+    return fail(JOLT_ERR_INVALID_ARG, "null batch array");
+  ca->codes[0] = (unsigned char*)c->k_codes_dev;
+  ca->codes[1] = (unsigned char*)c->v_codes_dev;
+  ca->scales[0] = (__half2*)c->k_scales_dev;
+  ca->scales[1] = (__half2*)c->v_scales_dev;
+  ca->bits[0] = c->bits_k;
+  ca->bits[1] = c->bits_v;
+  ca->H = c->n_heads;
+  ca->D = c->head_dim;
+  ca->n_pages = c->n_pages;
+  ca->page_shift = 0;
+  while ((1 << ca->page_shift) < c->page_size) ++ca->page_shift;
+  ba->table = b->page_table_dev;
+  ba->lens = b->lens_dev;
+  ba->starts = b->starts_dev;
+  ba->B = b->n_seqs;
+  ba->max_pages = b->max_pages;
+  ba->max_new = b->max_new;
+  ba->rows = b->n_rows;
+  ba->status = b->status_dev;
+  return JOLT_OK;
+}
+
+template <typename T>
+RowsArgs<T> rows_args(T* k, T* v, int64_t kr, int64_t kh, int64_t vr, int64_t vh) {
+  const int64_t per = 16 / sizeof(T);
+  RowsArgs<T> x;
+  x.x[0] = k;
+  x.x[1] = v;
+  x.row[0] = kr;
+  x.row[1] = vr;
+  x.head[0] = kh;
+  x.head[1] = vh;
+  x.vec[0] = aligned16(k) && kr % per == 0 && kh % per == 0;
+  x.vec[1] = aligned16(v) && vr % per == 0 && vh % per == 0;
+  return x;
+}
+
+template <typename T>
+jolt_status launch_write(const CacheArgs& c, const BatchArgs& a, const RowsArgs<const T>& x, cudaStream_t st) {
+  const long long blocks = (long long)a.rows * c.H * (c.D / pc::BLK);
+  count_launch(), cache_write_kernel<T><<<dim3((unsigned)ceil_div(blocks, 256), 2), 256, 0, st>>>(c, a, x);
+  CUDA_TRY(cudaGetLastError());
+  return JOLT_OK;
+}
+
+template <typename T>
+jolt_status launch_read(const CacheArgs& c, const BatchArgs& a, const RowsArgs<T>& x, cudaStream_t st) {
+  const long long blocks = (long long)a.rows * c.H * (c.D / pc::BLK);
+  count_launch(), cache_read_kernel<T><<<dim3((unsigned)ceil_div(blocks, 256), 2), 256, 0, st>>>(c, a, x);
+  CUDA_TRY(cudaGetLastError());
+  return JOLT_OK;
+}
+
+template <typename T>
+jolt_status launch_cache_attend(const CacheAttendArgs& A, cudaStream_t st) {
+  const dim3 grid(A.a.rows, A.nq);
+  if (A.c.D == 64) count_launch(), cache_attend_kernel<T, 64><<<grid, 64, 0, st>>>(A);
+  else count_launch(), cache_attend_kernel<T, 128><<<grid, 128, 0, st>>>(A);
+  CUDA_TRY(cudaGetLastError());
+  return JOLT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+jolt_status jolt_cache_write(const jolt_cache* cache, const jolt_cache_batch* batch, const void* k_dev,
+                             const void* v_dev, int32_t dtype, int64_t k_row_stride, int64_t k_head_stride,
+                             int64_t v_row_stride, int64_t v_head_stride, void* stream) {
+  CacheArgs c;
+  BatchArgs a;
+  JTRY(cache_args(cache, batch, &c, &a));
+  if (dtype != JOLT_BF16 && dtype != JOLT_F32 && dtype != JOLT_F16) return fail(JOLT_ERR_INVALID_ARG, "dtype %d", dtype);
+  if (a.B == 0 || a.rows == 0) return JOLT_OK;
+  if (!k_dev || !v_dev) return fail(JOLT_ERR_INVALID_ARG, "null rows");
+  cudaStream_t st = (cudaStream_t)stream;
+  ProfScope ps("cache_write", st, a.rows);
+  if (dtype == JOLT_BF16)
+    return launch_write(c, a, rows_args((const bf16*)k_dev, (const bf16*)v_dev, k_row_stride, k_head_stride,
+                                        v_row_stride, v_head_stride), st);
+  if (dtype == JOLT_F16)
+    return launch_write(c, a, rows_args((const __half*)k_dev, (const __half*)v_dev, k_row_stride, k_head_stride,
+                                        v_row_stride, v_head_stride), st);
+  return launch_write(c, a, rows_args((const float*)k_dev, (const float*)v_dev, k_row_stride, k_head_stride,
+                                      v_row_stride, v_head_stride), st);
+}
+
+jolt_status jolt_cache_read(const jolt_cache* cache, const jolt_cache_batch* batch, int32_t dtype, void* k_out_dev,
+                            void* v_out_dev, int64_t k_row_stride, int64_t k_head_stride, int64_t v_row_stride,
+                            int64_t v_head_stride, void* stream) {
+  CacheArgs c;
+  BatchArgs a;
+  JTRY(cache_args(cache, batch, &c, &a));
+  if (dtype != JOLT_BF16 && dtype != JOLT_F32 && dtype != JOLT_F16) return fail(JOLT_ERR_INVALID_ARG, "dtype %d", dtype);
+  if (a.B == 0 || a.rows == 0) return JOLT_OK;
+  if (!k_out_dev || !v_out_dev) return fail(JOLT_ERR_INVALID_ARG, "null rows");
+  cudaStream_t st = (cudaStream_t)stream;
+  ProfScope ps("cache_read", st, a.rows);
+  if (dtype == JOLT_BF16)
+    return launch_read(c, a, rows_args((bf16*)k_out_dev, (bf16*)v_out_dev, k_row_stride, k_head_stride, v_row_stride,
+                                       v_head_stride), st);
+  if (dtype == JOLT_F16)
+    return launch_read(c, a, rows_args((__half*)k_out_dev, (__half*)v_out_dev, k_row_stride, k_head_stride,
+                                       v_row_stride, v_head_stride), st);
+  return launch_read(c, a, rows_args((float*)k_out_dev, (float*)v_out_dev, k_row_stride, k_head_stride, v_row_stride,
+                                     v_head_stride), st);
+}
+
+jolt_status jolt_cache_attend_scratch_size(const jolt_cache* cache, const jolt_cache_batch* batch, int32_t n_q_heads,
+                                           size_t* bytes) {
+  CacheArgs c;
+  BatchArgs a;
+  JTRY(cache_args(cache, batch, &c, &a));
+  if (!bytes || n_q_heads < 1 || n_q_heads % c.H) return fail(JOLT_ERR_INVALID_ARG, "n_q_heads %d", n_q_heads);
+  *bytes = 256;
+  return JOLT_OK;
+}
+
+jolt_status jolt_cache_attend(const jolt_cache* cache, const jolt_cache_batch* batch,
+                              const jolt_cache_attend_options* opts, const void* q_dev, int32_t dtype,
+                              int32_t n_q_heads, int64_t q_row_stride, int64_t q_head_stride, void* out_dev,
+                              int64_t out_row_stride, int64_t out_head_stride, void* scratch_dev,
+                              size_t scratch_bytes, void* stream) {
+  CacheAttendArgs A;
+  JTRY(cache_args(cache, batch, &A.c, &A.a));
+  if (!opts) return fail(JOLT_ERR_INVALID_ARG, "null options");
+  if (dtype != JOLT_BF16 && dtype != JOLT_F16) return fail(JOLT_ERR_INVALID_ARG, "dtype %d of the queries", dtype);
+  size_t need = 0;
+  JTRY(jolt_cache_attend_scratch_size(cache, batch, n_q_heads, &need));
+  if (!(opts->scale >= 0.f) || !(opts->softcap >= 0.f) || std::isinf(opts->scale) || std::isinf(opts->softcap))
+    return fail(JOLT_ERR_INVALID_ARG, "scale %g, softcap %g", opts->scale, opts->softcap);
+  if (opts->window < 0) return fail(JOLT_ERR_INVALID_ARG, "window %d", opts->window);
+  if (opts->mask_dev && (opts->mask_words < 1 || opts->mask_words < ceil_div(A.a.max_new, 32)))
+    return fail(JOLT_ERR_INVALID_ARG, "mask_words %d for %d new rows", opts->mask_words, A.a.max_new);
+  if ((opts->prefix_out_dev == nullptr) != (opts->prefix_lse_dev == nullptr))
+    return fail(JOLT_ERR_INVALID_ARG, "give both or neither of prefix_out, prefix_lse");
+  if (A.a.B == 0 || A.a.rows == 0 || A.a.max_new == 0) return JOLT_OK;
+  if (!q_dev || !out_dev || !scratch_dev) return fail(JOLT_ERR_INVALID_ARG, "null pointer");
+  if (scratch_bytes < need)
+    return fail(JOLT_ERR_WORKSPACE_TOO_SMALL, "cache attend scratch %zu bytes, need %zu", scratch_bytes, need);
+  if (reinterpret_cast<uintptr_t>(scratch_dev) % 256) return fail(JOLT_ERR_INVALID_ARG, "scratch not 256-byte aligned");
+  A.nq = n_q_heads;
+  A.G = n_q_heads / A.c.H;
+  A.scale = opts->scale > 0.f ? opts->scale : (float)(1.0 / sqrt((double)A.c.D));
+  A.cap = opts->softcap;
+  A.window = opts->window;
+  A.words = opts->mask_words;
+  A.slopes = opts->slopes_dev;
+  A.positions = opts->positions_dev;
+  A.mask = opts->mask_dev;
+  A.prefix_out = opts->prefix_out_dev;
+  A.prefix_lse = opts->prefix_lse_dev;
+  A.q = q_dev;
+  A.q_row = q_row_stride;
+  A.q_head = q_head_stride;
+  A.out = out_dev;
+  A.o_row = out_row_stride;
+  A.o_head = out_head_stride;
+  cudaStream_t st = (cudaStream_t)stream;
+  ProfScope ps("cache_attend", st, A.a.rows);
+  return dtype == JOLT_BF16 ? launch_cache_attend<bf16>(A, st) : launch_cache_attend<__half>(A, st);
+}
+
+jolt_status jolt_cache_check(const uint32_t* status_dev, void* stream) {
+  if (!status_dev) return fail(JOLT_ERR_INVALID_ARG, "null status word");
+  uint32_t h = 0;
+  cudaStream_t st = (cudaStream_t)stream;
+  CUDA_TRY(cudaMemcpyAsync(&h, status_dev, sizeof h, cudaMemcpyDeviceToHost, st));
+  CUDA_TRY(cudaStreamSynchronize(st));
+  if (h & DEV_ERR_TIMEOUT) return fail(JOLT_ERR_TIMEOUT, "a bounded device-side wait gave up");
+  if (h & DEV_ERR_BATCH) return fail(JOLT_ERR_INVALID_ARG, "a batch named rows, lengths or pages that do not exist");
+  if (h & DEV_ERR_NONFINITE) return fail(JOLT_ERR_NUMERIC, "NaN or values beyond fp16 among the rows written");
+  if (h) return fail(JOLT_ERR_CUDA, "unexpected device status %u", h);
+  return JOLT_OK;
+}
+
+}  // extern "C"

@@ -38,6 +38,7 @@ enum : uint32_t {
   DEV_ERR_BLOB = 8u,          // a compressed record failed validation
   DEV_ERR_CAPACITY = 16u,     // output buffer smaller than the chosen payload
   DEV_ERR_TIMEOUT = 32u,      // a bounded device-side wait gave up
+  DEV_ERR_BATCH = 64u,        // a paged batch names rows, lengths or pages that do not exist
 };
 
 // ---- splitmix64 (Steele, Lea & Flood, OOPSLA 2014) ------------------------------------

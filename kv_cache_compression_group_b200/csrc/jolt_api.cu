@@ -10,6 +10,7 @@
 
 #include "jolt.h"
 #include "common.cuh"
+#include "host.cuh"
 #include "gemm.cuh"
 #include "kernels.cuh"
 #include "misc.cuh"
@@ -24,34 +25,11 @@ using namespace jolt;
 
 namespace {
 
-thread_local std::string g_err;
-
-jolt_status fail(jolt_status s, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return s;
-}
-
-#define CUDA_TRY(x)                                                                         \
-  do {                                                                                      \
-    cudaError_t e_ = (x);                                                                   \
-    if (e_ != cudaSuccess) return fail(JOLT_ERR_CUDA, "%s: %s", #x, cudaGetErrorString(e_)); \
-  } while (0)
 #define SOLVER_TRY(x)                                                               \
   do {                                                                              \
     cusolverStatus_t s_ = (x);                                                      \
     if (s_ != CUSOLVER_STATUS_SUCCESS) return fail(JOLT_ERR_CUDA, "%s: cusolver status %d", #x, (int)s_); \
   } while (0)
-#define JTRY(x)                    \
-  do {                             \
-    jolt_status j_ = (x);          \
-    if (j_ != JOLT_OK) return j_;  \
-  } while (0)
-
 // ------------------------------------------------------------------------------------------
 // cuSOLVER handle (one per thread and device)
 // ------------------------------------------------------------------------------------------
@@ -105,61 +83,8 @@ jolt_status aux_get(Aux** out) {
 }
 
 // ------------------------------------------------------------------------------------------
-// optional stage timing: CUDA events recorded around each stage on the launch stream
-// ------------------------------------------------------------------------------------------
-struct ProfRec {
-  std::string name;
-  cudaEvent_t a, b;
-  long long units;  // work items the stage processed (for per-launch figures)
-};
-struct Profiler {
-  bool on = false;
-  std::vector<ProfRec> recs;
-  std::vector<cudaEvent_t> pool;
-  cudaEvent_t get() {
-    if (!pool.empty()) {
-      cudaEvent_t e = pool.back();
-      pool.pop_back();
-      return e;
-    }
-    cudaEvent_t e;
-    cudaEventCreate(&e);
-    return e;
-  }
-};
-thread_local Profiler g_prof;
-
-struct ProfScope {
-  ProfRec rec;
-  cudaStream_t st;
-  bool on;
-  ProfScope(const char* name, cudaStream_t s, long long units = 1) : st(s), on(g_prof.on) {
-    if (!on) return;
-    rec.name = name;
-    rec.units = units;
-    rec.a = g_prof.get();
-    rec.b = g_prof.get();
-    cudaEventRecord(rec.a, st);
-  }
-  ~ProfScope() {
-    if (!on) return;
-    cudaEventRecord(rec.b, st);
-    g_prof.recs.push_back(rec);
-  }
-};
-
-// ------------------------------------------------------------------------------------------
 // plan: derived sizes and workspace layout
 // ------------------------------------------------------------------------------------------
-struct Bump {
-  size_t off = 0;
-  size_t take(size_t bytes) {
-    size_t o = off;
-    off += (bytes + 255) / 256 * 256;
-    return o;
-  }
-};
-
 // Cholesky QR runs its Gram and its triangular product on the tensor cores for block widths
 // of at least QR_TC_MINK columns; a Gram partial sums QR_TC_CHUNK rows in fp32
 constexpr int QR_TC_MINK = 64;
@@ -2361,27 +2286,10 @@ jolt_status launch_attend(const AttendArgs& a, cudaStream_t st) {
   CUDA_TRY(cudaGetLastError());
   return JOLT_OK;
 }
-}  // namespace
 
-extern "C" {
-
-jolt_status jolt_attend_prepare(const void* blob_dev, void* ws_dev, size_t ws_bytes, void* stream) {
-  if (!blob_dev || !ws_dev) return fail(JOLT_ERR_INVALID_ARG, "null pointer");
-  Prepared pr;
-  return decode_prepare(blob_dev, ws_dev, ws_bytes, (cudaStream_t)stream, &pr, true);
-}
-
-jolt_status jolt_attend_scratch_size(const jolt_shape* shape, int32_t max_token_rank, int32_t n_q_heads,
-                                     size_t* bytes) {
-  if (!shape || !bytes || n_q_heads < 1 || max_token_rank < 1) return fail(JOLT_ERR_INVALID_ARG, "attend sizes");
-  if (shape->n_heads < 1 || n_q_heads % shape->n_heads) return fail(JOLT_ERR_INVALID_ARG, "n_q_heads % n_heads");
-  const int rT = (int)round_up(max_token_rank, 8);
-  *bytes = attend_scratch(shape->n_tokens, shape->n_heads, shape->head_dim, rT, n_q_heads);
-  return JOLT_OK;
-}
-
-jolt_status jolt_attend(const void* blob_dev, const void* ws_dev, size_t ws_bytes, int32_t layer, const float* q_dev,
-                        int32_t n_q_heads, float* out_dev, void* scratch_dev, size_t scratch_bytes, void* stream) {
+jolt_status attend_with(const void* blob_dev, const void* ws_dev, size_t ws_bytes, int32_t layer, const float* q_dev,
+                        int32_t n_q_heads, float* out_dev, float* lse_dev, void* scratch_dev, size_t scratch_bytes,
+                        void* stream) {
   if (!blob_dev || !ws_dev || !q_dev || !out_dev || !scratch_dev) return fail(JOLT_ERR_INVALID_ARG, "null pointer");
   cudaStream_t st = (cudaStream_t)stream;
   Prepared pr;
@@ -2422,6 +2330,7 @@ jolt_status jolt_attend(const void* blob_dev, const void* ws_dev, size_t ws_byte
   a.part = a.a + (size_t)n_q_heads * p.rTmax;
   a.nch = attend_chunks(p.T, p.H);
   a.out = out_dev;
+  a.lse = lse_dev;
   ProfScope ps("attend", st, 1);
   switch (p.D) {
     case 16: return launch_attend<16>(a, st);
@@ -2429,6 +2338,38 @@ jolt_status jolt_attend(const void* blob_dev, const void* ws_dev, size_t ws_byte
     case 64: return launch_attend<64>(a, st);
     default: return launch_attend<128>(a, st);
   }
+}
+}  // namespace
+
+extern "C" {
+
+jolt_status jolt_attend_prepare(const void* blob_dev, void* ws_dev, size_t ws_bytes, void* stream) {
+  if (!blob_dev || !ws_dev) return fail(JOLT_ERR_INVALID_ARG, "null pointer");
+  Prepared pr;
+  return decode_prepare(blob_dev, ws_dev, ws_bytes, (cudaStream_t)stream, &pr, true);
+}
+
+jolt_status jolt_attend_scratch_size(const jolt_shape* shape, int32_t max_token_rank, int32_t n_q_heads,
+                                     size_t* bytes) {
+  if (!shape || !bytes || n_q_heads < 1 || max_token_rank < 1) return fail(JOLT_ERR_INVALID_ARG, "attend sizes");
+  if (shape->n_heads < 1 || n_q_heads % shape->n_heads) return fail(JOLT_ERR_INVALID_ARG, "n_q_heads % n_heads");
+  const int rT = (int)round_up(max_token_rank, 8);
+  *bytes = attend_scratch(shape->n_tokens, shape->n_heads, shape->head_dim, rT, n_q_heads);
+  return JOLT_OK;
+}
+
+jolt_status jolt_attend(const void* blob_dev, const void* ws_dev, size_t ws_bytes, int32_t layer, const float* q_dev,
+                        int32_t n_q_heads, float* out_dev, void* scratch_dev, size_t scratch_bytes, void* stream) {
+  return attend_with(blob_dev, ws_dev, ws_bytes, layer, q_dev, n_q_heads, out_dev, nullptr, scratch_dev, scratch_bytes,
+                     stream);
+}
+
+jolt_status jolt_attend_state(const void* blob_dev, const void* ws_dev, size_t ws_bytes, int32_t layer,
+                              const float* q_dev, int32_t n_q_heads, float* out_dev, float* lse_dev,
+                              void* scratch_dev, size_t scratch_bytes, void* stream) {
+  if (!lse_dev) return fail(JOLT_ERR_INVALID_ARG, "null pointer");
+  return attend_with(blob_dev, ws_dev, ws_bytes, layer, q_dev, n_q_heads, out_dev, lse_dev, scratch_dev, scratch_bytes,
+                     stream);
 }
 
 jolt_status jolt_quant_baseline(const jolt_shape* shape, const void* k_dev, const void* v_dev, int32_t bits,

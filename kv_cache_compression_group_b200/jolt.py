@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libjolt.so")
 
 MAXC = 8
-JOLT_BF16, JOLT_F32 = 0, 1
+JOLT_BF16, JOLT_F32, JOLT_F16 = 0, 1, 2
 JOLT_EXACT, JOLT_RANDOMIZED = 0, 1
 
 STATUS_NAMES = {
@@ -30,6 +30,8 @@ EXPORTED = [
     "jolt_decompress", "jolt_frobenius", "jolt_profile_begin", "jolt_profile_end", "jolt_recon_operator",
     "jolt_launch_count", "jolt_frobenius_noalloc", "jolt_set_graphs", "jolt_release", "jolt_fp32_rate_probe",
     "jolt_wait_selftest", "jolt_attend_prepare", "jolt_attend_scratch_size", "jolt_attend", "jolt_quant_baseline",
+    "jolt_attend_state", "jolt_cache_write", "jolt_cache_read", "jolt_cache_attend_scratch_size", "jolt_cache_attend",
+    "jolt_cache_check",
 ]
 
 
@@ -60,6 +62,25 @@ class CUnitRecord(ctypes.Structure):
                 ("distortion", ctypes.c_double)]
 
 
+class CCache(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("bits_k", ctypes.c_int32), ("bits_v", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p)]
+
+
+class CCacheBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("n_rows", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class CAttendOptions(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("mask_words", ctypes.c_int32), ("slopes", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("prefix_out", ctypes.c_void_p), ("prefix_lse", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -72,6 +93,8 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         vp, sz, i32, u64, pS, pO = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_uint64,
                                     ctypes.POINTER(CShape), ctypes.POINTER(COptions))
+        i64, pC, pB, pA = (ctypes.c_int64, ctypes.POINTER(CCache), ctypes.POINTER(CCacheBatch),
+                           ctypes.POINTER(CAttendOptions))
         L.jolt_version.restype = ctypes.c_char_p
         L.jolt_last_error.restype = ctypes.c_char_p
         sigs = {
@@ -98,6 +121,12 @@ def lib():
             "jolt_attend_scratch_size": [pS, i32, i32, ctypes.POINTER(sz)],
             "jolt_attend": [vp, vp, sz, i32, vp, i32, vp, vp, sz, vp],
             "jolt_quant_baseline": [pS, vp, vp, i32, vp, vp, vp, vp, sz, vp],
+            "jolt_attend_state": [vp, vp, sz, i32, vp, i32, vp, vp, vp, sz, vp],
+            "jolt_cache_write": [pC, pB, vp, vp, i32, i64, i64, i64, i64, vp],
+            "jolt_cache_read": [pC, pB, i32, vp, vp, i64, i64, i64, i64, vp],
+            "jolt_cache_attend_scratch_size": [pC, pB, i32, ctypes.POINTER(sz)],
+            "jolt_cache_attend": [pC, pB, pA, vp, i32, i32, i64, i64, vp, i64, i64, vp, sz, vp],
+            "jolt_cache_check": [vp, vp],
         }
         L.jolt_launch_count.argtypes = []
         L.jolt_launch_count.restype = ctypes.c_uint64
@@ -341,6 +370,202 @@ class Attention:
         _check(lib().jolt_attend(_ptr(self.blob), self.ws_ptr, self.ws_bytes, int(layer), _ptr(q), self.nq, _ptr(out),
                                  _ptr(self.scratch), self.scratch.numel(), _stream(stream)))
         return out
+
+    def attend_state(self, layer: int, q: torch.Tensor, stream=None):
+        """As attend, with the log-sum-exp of the scores: (output, lse [n_q_heads] fp32), the prefix
+        that QuantCache.attend joins to its own keys."""
+        q = q.to(torch.float32).contiguous()
+        if q.shape != (self.nq, self.D):
+            raise ValueError(f"q must be [{self.nq}, {self.D}]")
+        out = torch.empty_like(q)
+        lse = torch.empty(self.nq, dtype=torch.float32, device=q.device)
+        _check(lib().jolt_attend_state(_ptr(self.blob), self.ws_ptr, self.ws_bytes, int(layer), _ptr(q), self.nq,
+                                       _ptr(out), _ptr(lse), _ptr(self.scratch), self.scratch.numel(),
+                                       _stream(stream)))
+        return out, lse
+
+
+_CACHE_DTYPES = {torch.bfloat16: JOLT_BF16, torch.float32: JOLT_F32, torch.float16: JOLT_F16}
+
+
+class CacheBatch:
+    """A ragged batch over paged caches: rows starts[b] .. starts[b + 1] - 1 of a call's tensors are
+    the last rows of sequence b, whose length with them is lens[b]; position t of it is slot
+    t % page_size of page page_table[b, t // page_size].
+
+    page_table [n_seqs, max_pages], lens [n_seqs] and starts [n_seqs + 1] are int32 tensors on the
+    device, kept (not copied): they are read when a call's kernels run, so a captured graph sees
+    what is later written into them.  max_new bounds the rows of one sequence."""
+
+    def __init__(self, page_table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor, max_new: int):
+        for name, t, dim in (("page_table", page_table, 2), ("lens", lens, 1), ("starts", starts, 1)):
+            if t.dtype != torch.int32 or t.dim() != dim or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {dim} dimensions")
+            if t.device != page_table.device:
+                raise ValueError("page_table, lens and starts must be on one device")
+        if lens.shape[0] != page_table.shape[0] or starts.shape[0] != lens.shape[0] + 1:
+            raise ValueError("page_table [n_seqs, max_pages], lens [n_seqs] and starts [n_seqs + 1] are needed")
+        if max_new < 0:
+            raise ValueError("max_new must not be negative")
+        self.page_table, self.lens, self.starts, self.max_new = page_table, lens, starts, int(max_new)
+        self.device = page_table.device
+        self._c = CCacheBatch(lens.shape[0], page_table.shape[1], self.max_new, 0, page_table.data_ptr(),
+                              lens.data_ptr(), starts.data_ptr(), 0)
+
+
+class QuantCache:
+    """Pages of block-quantised keys and values for every layer of a model, written row by row.
+
+    pools: (k_codes, k_scales, v_codes, v_scales) to use, else they are allocated (and zeroed):
+    codes uint8 [n_layers, n_pages, n_heads, page_size, head_dim * bits / 8], scales fp16
+    [n_layers, n_pages, n_heads, page_size, head_dim / 16, 2].  bits: of K and V, each 2, 4 or 8.
+    The errors that only the device sees (a batch naming rows or pages that do not exist, NaN
+    among the rows) collect in a status word that check() reads."""
+
+    def __init__(self, n_layers, n_heads, head_dim, n_pages, page_size=64, bits=(4, 4), device="cuda", pools=None):
+        bits = (bits, bits) if isinstance(bits, int) else tuple(bits)
+        if len(bits) != 2:
+            raise ValueError("bits is one bit-width or (bits of K, bits of V)")
+        if min(n_layers, n_heads, n_pages) < 1:
+            raise ValueError("n_layers, n_heads and n_pages must be positive")
+        want = []
+        for b in bits:
+            want += [(n_layers, n_pages, n_heads, page_size, head_dim * b // 8),
+                     (n_layers, n_pages, n_heads, page_size, head_dim // 16, 2)]
+        if pools is None:
+            pools = tuple(torch.zeros(shape, dtype=torch.float16 if i % 2 else torch.uint8, device=device)
+                          for i, shape in enumerate(want))
+        names = ("k_codes", "k_scales", "v_codes", "v_scales")
+        if len(pools) != 4:
+            raise ValueError("pools are (k_codes, k_scales, v_codes, v_scales)")
+        for i, (name, t) in enumerate(zip(names, pools)):
+            dt = torch.float16 if i % 2 else torch.uint8
+            if tuple(t.shape) != want[i] or t.dtype != dt or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dt} CUDA tensor of shape {want[i]}")
+            if t.device != pools[0].device:
+                raise ValueError("the pools must be on one device")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = pools
+        self.n_layers, self.n_heads, self.head_dim = n_layers, n_heads, head_dim
+        self.n_pages, self.page_size, self.bits = n_pages, page_size, bits
+        self.device = pools[0].device
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._layers = []
+        for layer in range(n_layers):
+            self._layers.append(CCache(n_heads, head_dim, page_size, n_pages, bits[0], bits[1],
+                                       *(t[layer].data_ptr() for t in pools)))
+        # the shape is checked now rather than at the first call
+        nbytes = ctypes.c_size_t()
+        with torch.cuda.device(self.device):
+            _check(lib().jolt_cache_attend_scratch_size(ctypes.byref(self._layers[0]), ctypes.byref(CCacheBatch()),
+                                                        n_heads, ctypes.byref(nbytes)))
+
+    def _call(self, layer, batch, rows, tensors, stream):
+        """The layer's pool, the batch for this many rows, and the stream of a call."""
+        if not 0 <= layer < self.n_layers:
+            raise ValueError(f"layer {layer} not in [0, {self.n_layers})")
+        for t in (batch, *tensors):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"everything must be on the cache's device {self.device}")
+        b = CCacheBatch.from_buffer_copy(batch._c)
+        b.n_rows, b.status = rows, self.status.data_ptr()
+        return self._layers[layer], b, torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def _rows(self, t, name, heads):
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
+            raise ValueError(f"{name} must be [rows, {heads}, {self.head_dim}]")
+        if t.shape[0] and t.stride(2) != 1:
+            raise ValueError(f"the features of {name} must be contiguous")
+        return t
+
+    def write(self, layer: int, k: torch.Tensor, v: torch.Tensor, batch: CacheBatch, stream=None):
+        """Quantise rows k, v [rows, n_heads, head_dim] (bf16, fp16 or fp32, strided rows and heads)
+        into their pages: they become the last rows of the batch's sequences."""
+        self._rows(k, "k", self.n_heads)
+        self._rows(v, "v", self.n_heads)
+        if k.dtype != v.dtype or k.shape != v.shape or k.dtype not in _CACHE_DTYPES:
+            raise ValueError("k and v must have one shape and one of the types bf16, fp16, fp32")
+        c, b, st = self._call(layer, batch, k.shape[0], (k, v), stream)
+        with torch.cuda.device(self.device):
+            _check(lib().jolt_cache_write(c, b, k.data_ptr(), v.data_ptr(), _CACHE_DTYPES[k.dtype], k.stride(0),
+                                          k.stride(1), v.stride(0), v.stride(1), _stream(st)))
+
+    def read(self, layer: int, batch: CacheBatch, rows: int, dtype=torch.bfloat16, out=None, stream=None):
+        """The batch's rows as dense (k, v), each [rows, n_heads, head_dim] of dtype; out: tensors to
+        write into (rows that belong to no sequence are left as they are)."""
+        if dtype not in _CACHE_DTYPES:
+            raise ValueError("dtype must be bf16, fp16 or fp32")
+        if out is None:
+            shape = (int(rows), self.n_heads, self.head_dim)
+            out = tuple(torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+        k, v = out
+        self._rows(k, "out[0]", self.n_heads)
+        self._rows(v, "out[1]", self.n_heads)
+        if k.dtype != dtype or v.dtype != dtype or k.shape != v.shape or k.shape[0] != rows:
+            raise ValueError("out must be two tensors of dtype and rows")
+        c, b, st = self._call(layer, batch, k.shape[0], (k, v), stream)
+        with torch.cuda.device(self.device):
+            _check(lib().jolt_cache_read(c, b, _CACHE_DTYPES[dtype], k.data_ptr(), v.data_ptr(), k.stride(0),
+                                         k.stride(1), v.stride(0), v.stride(1), _stream(st)))
+        return k, v
+
+    def attend(self, layer: int, q: torch.Tensor, batch: CacheBatch, scale: float = 0.0, softcap: float = 0.0,
+               window: int = 0, slopes=None, positions=None, mask=None, prefix=None, out=None, stream=None):
+        """Attention of rows q [rows, n_q_heads, head_dim] (bf16 or fp16), whose keys and values are
+        written already, over their sequences; returns the output, in q's type.
+
+        scale: of q . k, 0 for 1 / sqrt(head_dim).  softcap c > 0: scores c tanh(s / c).
+        window w > 0: positions above p - w only.  slopes [n_q_heads] fp32: scores minus
+        slope * (p_query - p_key).  positions [rows] int32: of the new rows where they are not
+        their places (a tree: the depths).  mask [rows, words] int32: bit j of row i set if it sees
+        new row j of its sequence, for a tree of drafted tokens (itself and its ancestors); causal
+        without.  prefix: (out [rows, n_q_heads, head_dim], lse [rows, n_q_heads]) fp32 of the same
+        queries over other keys (Attention.attend_state), joined to the output."""
+        if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % self.n_heads:
+            raise ValueError(f"q must be [rows, a multiple of {self.n_heads} heads, {self.head_dim}]")
+        rows, nq = q.shape[0], q.shape[1]
+        self._rows(q, "q", nq)
+        if q.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("q must be bf16 or fp16")
+        p_out, p_lse = prefix if prefix is not None else (None, None)
+        for name, t, shape, dt in (("slopes", slopes, (nq,), torch.float32),
+                                   ("positions", positions, (rows,), torch.int32),
+                                   ("mask", mask, None, torch.int32),
+                                   ("prefix[0]", p_out, (rows, nq, self.head_dim), torch.float32),
+                                   ("prefix[1]", p_lse, (rows, nq), torch.float32)):
+            if t is None:
+                continue
+            if t.dtype != dt or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape or '[rows, words]'}")
+        if mask is not None and (mask.dim() != 2 or mask.shape[0] != rows):
+            raise ValueError("mask must be [rows, words]")
+        c, b, st = self._call(layer, batch, rows, (q, slopes, positions, mask, p_out, p_lse, out), stream)
+        with torch.cuda.device(self.device):
+            if out is None:
+                out = torch.empty((rows, nq, self.head_dim), dtype=q.dtype, device=self.device)
+            elif out.shape != q.shape or out.dtype != q.dtype:
+                raise ValueError("out must have q's shape and type")
+            self._rows(out, "out", nq)
+            nbytes = ctypes.c_size_t()
+            _check(lib().jolt_cache_attend_scratch_size(c, b, nq, ctypes.byref(nbytes)))
+            # a scratch of its own for every call: two calls, or two captured graphs, never share one
+            scratch = torch.empty(nbytes.value, dtype=torch.uint8, device=self.device)
+            o = CAttendOptions(scale, softcap, window, 0 if mask is None else mask.shape[1],
+                               *(None if t is None else t.data_ptr() for t in (slopes, positions, mask, p_out, p_lse)))
+            _check(lib().jolt_cache_attend(c, b, o, q.data_ptr(), _CACHE_DTYPES[q.dtype], nq, q.stride(0),
+                                           q.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
+                                           scratch.data_ptr(), nbytes.value, _stream(st)))
+            if stream is not None and isinstance(stream, torch.cuda.Stream):
+                scratch.record_stream(stream)
+        return out
+
+    def check(self, stream=None):
+        """Raise what the kernels of this cache's calls found so far (synchronises), and clear it."""
+        with torch.cuda.device(self.device):
+            st = torch.cuda.current_stream(self.device) if stream is None else stream
+            status = lib().jolt_cache_check(self.status.data_ptr(), _stream(st))
+            if status:
+                self.status.zero_()
+            _check(status)
 
 
 def read_header(blob: torch.Tensor, stream=None):

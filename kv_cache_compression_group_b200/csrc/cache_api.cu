@@ -86,11 +86,78 @@ jolt_status launch_read(const CacheArgs& c, const BatchArgs& a, const RowsArgs<T
   return JOLT_OK;
 }
 
-template <typename T>
+// rows of one KV head that the narrow kernel takes; more go to the other one
+constexpr int FEW_ROWS = 32;
+
+// n-tiles of the narrow kernel for at most `rows` rows of a KV head
+int few_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+// shared memory of the narrow kernel, and its blocks: as many as the GPU holds at once (by
+// registers 4, 3 or 2 per SM, by shared memory what 228 KB hold with 1 KB reserved for each)
+int few_smem(const CacheArgs& c, int nt) {
+  const int bk = c.bits[0], bv = c.bits[1];
+  if (c.D == 64)
+    return nt == 1 ? ca::Smem<64, 1>::bytes(bk, bv) : nt == 2 ? ca::Smem<64, 2>::bytes(bk, bv) : ca::Smem<64, 4>::bytes(bk, bv);
+  return nt == 1 ? ca::Smem<128, 1>::bytes(bk, bv) : nt == 2 ? ca::Smem<128, 2>::bytes(bk, bv) : ca::Smem<128, 4>::bytes(bk, bv);
+}
+int few_blocks(const CacheArgs& c, int nt) {
+  const int by_regs = nt == 1 ? 4 : nt == 2 ? 3 : 2, by_smem = 228 * 1024 / (few_smem(c, nt) + 1024);
+  return 148 * (by_regs < by_smem ? by_regs : by_smem);
+}
+
+struct Scratch {
+  size_t notes, pieces, total;
+};
+Scratch attend_scratch(const CacheArgs& c, const BatchArgs& a, int nq) {
+  const long long rows = (long long)a.max_new * (nq / c.H);
+  Scratch s{0, 0, 256};
+  if (rows > FEW_ROWS) return s;
+  Bump m;
+  const int nt = few_tiles(rows), blocks = few_blocks(c, nt);
+  s.notes = m.take(sizeof(int4) * 2 * blocks);
+  s.pieces = m.take(sizeof(float) * 2 * blocks * 8 * nt * (c.D + 4));
+  s.total = m.off;
+  return s;
+}
+
+// launch with programmatic stream serialization: the join's blocks may be scheduled while the
+// last blocks of the kernel before it run; they wait for its end before they read
+template <typename K>
+cudaError_t launch_after(K kernel, dim3 grid, int threads, const CacheAttendArgs& A, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, A);
+}
+
+template <int D, int NT>
+jolt_status launch_few(const CacheAttendArgs& A, cudaStream_t st) {
+  const int smem = few_smem(A.c, NT), blocks = few_blocks(A.c, NT);
+  CUDA_TRY(cudaFuncSetAttribute(cache_few_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  count_launch(), cache_few_rows_kernel<D, NT><<<blocks, ca::WARPS * 32, smem, st>>>(A);
+  CUDA_TRY(cudaGetLastError());
+  CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT>, dim3(blocks, A.a.max_new * A.G), 256, A, st));
+  return JOLT_OK;
+}
+
+template <int D>
 jolt_status launch_cache_attend(const CacheAttendArgs& A, cudaStream_t st) {
-  const dim3 grid(A.a.rows, A.nq);
-  if (A.c.D == 64) count_launch(), cache_attend_kernel<T, 64><<<grid, 64, 0, st>>>(A);
-  else count_launch(), cache_attend_kernel<T, 128><<<grid, 128, 0, st>>>(A);
+  const long long rows = (long long)A.a.max_new * A.G;
+  if (rows <= FEW_ROWS) {
+    switch (few_tiles(rows)) {
+      case 1: return launch_few<D, 1>(A, st);
+      case 2: return launch_few<D, 2>(A, st);
+      default: return launch_few<D, 4>(A, st);
+    }
+  }
+  count_launch(), cache_attend_kernel<D><<<dim3(A.a.rows, A.nq), D, 0, st>>>(A);
   CUDA_TRY(cudaGetLastError());
   return JOLT_OK;
 }
@@ -147,7 +214,7 @@ jolt_status jolt_cache_attend_scratch_size(const jolt_cache* cache, const jolt_c
   BatchArgs a;
   JTRY(cache_args(cache, batch, &c, &a));
   if (!bytes || n_q_heads < 1 || n_q_heads % c.H) return fail(JOLT_ERR_INVALID_ARG, "n_q_heads %d", n_q_heads);
-  *bytes = 256;
+  *bytes = attend_scratch(c, a, n_q_heads).total;
   return JOLT_OK;
 }
 
@@ -185,7 +252,11 @@ jolt_status jolt_cache_attend(const jolt_cache* cache, const jolt_cache_batch* b
   A.mask = opts->mask_dev;
   A.prefix_out = opts->prefix_out_dev;
   A.prefix_lse = opts->prefix_lse_dev;
+  const Scratch at = attend_scratch(A.c, A.a, n_q_heads);
+  A.notes = reinterpret_cast<int4*>((unsigned char*)scratch_dev + at.notes);
+  A.pieces = reinterpret_cast<float*>((unsigned char*)scratch_dev + at.pieces);
   A.q = q_dev;
+  A.q_f16 = dtype == JOLT_F16;
   A.q_row = q_row_stride;
   A.q_head = q_head_stride;
   A.out = out_dev;
@@ -193,7 +264,7 @@ jolt_status jolt_cache_attend(const jolt_cache* cache, const jolt_cache_batch* b
   A.o_head = out_head_stride;
   cudaStream_t st = (cudaStream_t)stream;
   ProfScope ps("cache_attend", st, A.a.rows);
-  return dtype == JOLT_BF16 ? launch_cache_attend<bf16>(A, st) : launch_cache_attend<__half>(A, st);
+  return A.c.D == 64 ? launch_cache_attend<64>(A, st) : launch_cache_attend<128>(A, st);
 }
 
 jolt_status jolt_cache_check(const uint32_t* status_dev, void* stream) {

@@ -1,0 +1,150 @@
+// How attention over the paged cache is split over thread blocks, and how the pieces are joined.
+//
+// A job is one KV head of one sequence (and, for long chunks, one tile of its rows); its keys are
+// cut into units of a fixed number of tokens.  All units of all jobs, in order, are dealt out to
+// the thread blocks in equal contiguous ranges, so a ragged batch and one long sequence load the
+// GPU alike.  A job that one block has from its first unit to its last is finished there.  Of any
+// other job every block leaves a piece (running maximum, sum, and unnormalised output of every
+// row) in the scratch: in its slot 1 the job that begins in it, in its slot 0 the job that does
+// not.  The block in which a job begins also leaves a note of it, and a second kernel joins the
+// pieces of every noted job in their order, so results are the same in every run.
+#pragma once
+
+#include "cache.cuh"
+
+namespace jolt {
+
+struct CacheAttendArgs {
+  CacheArgs c;
+  BatchArgs a;
+  int nq, G;                 // query heads, query heads per KV head
+  float scale, cap;          // cap 0: none
+  int window;                // 0: none
+  int words;
+  const float* slopes;
+  const int* positions;
+  const uint32_t* mask;
+  const float* prefix_out;
+  const float* prefix_lse;
+  const void* q;
+  int q_f16;                 // queries and outputs are fp16, else bf16
+  long long q_row, q_head;
+  void* out;
+  long long o_row, o_head;
+  // scratch
+  int4* notes;               // [blocks][2]: {sequence, KV head, row tile or -1, -}, {units in all, end of the job}
+  float* pieces;             // [blocks][2][rows of a tile][D + 4]: D outputs, maximum, sum
+};
+
+namespace cs {
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float MASKED = -INFINITY;
+// Weights are 2^(s - m + SHIFT): fp16 holds them normalised over 21 binary orders below the
+// maximum, and the reference m may lag behind the true maximum by 2^LAG before the sums are
+// rescaled (SHIFT + LAG = 15 keeps them below fp16's largest).
+constexpr float SHIFT = 7.f, LAG = 8.f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// start of block c's range when `total` units are dealt to `parts` blocks
+__device__ __forceinline__ long long range_start(long long total, int parts, int c) { return total * c / parts; }
+}  // namespace cs
+
+// position of key t of a sequence whose new rows start at position `old` and row `row0`
+__device__ __forceinline__ int key_position(const CacheAttendArgs& A, int row0, int old, int t) {
+  return (A.positions && t >= old) ? A.positions[row0 + t - old] : t;
+}
+
+// whether row i (of n, at position pq) sees key t (at position pk)
+__device__ __forceinline__ bool row_sees(const CacheAttendArgs& A, int row0, int old, int n, int i, int pq, int t,
+                                         int pk) {
+  if (A.window && (pq - pk >= A.window || t <= old - A.window)) return false;
+  const int j = t - old;
+  if (j < 0) return true;
+  if (j >= n) return false;
+  if (!A.mask) return j <= i;
+  return (A.mask[(long long)(row0 + i) * A.words + (j >> 5)] >> (j & 31)) & 1u;
+}
+
+// s = cap tanh(s / cap), with tanh x = 1 - 2 / (e^(2x) + 1)
+__device__ __forceinline__ float cap_score(float s, float cap) {
+  const float e = cs::ex2(2.f * cs::LOG2E / cap * s);
+  return cap - __fdividef(2.f * cap, e + 1.f);
+}
+
+__device__ __forceinline__ float ld_q(const CacheAttendArgs& A, long long at) {
+  return A.q_f16 ? __half2float(reinterpret_cast<const __half*>(A.q)[at])
+                 : __bfloat162float(reinterpret_cast<const bf16*>(A.q)[at]);
+}
+
+// Output element (row r, query head j, feature d): the joined sums o / l with reference maximum m
+// (base 2), together with the row's prefix if there is one.  A row that saw nothing has l = 0.
+__device__ __forceinline__ void store_out(const CacheAttendArgs& A, int D, int r, int j, int d, float o, float l,
+                                          float m) {
+  if (A.prefix_out) {
+    const float lp = A.prefix_lse[(long long)r * A.nq + j] * cs::LOG2E, top = fmaxf(m, lp);
+    const float f = l == 0.f ? 0.f : cs::ex2(m - top);
+    const float g = lp == -INFINITY ? 0.f : cs::ex2(lp - top + cs::SHIFT);
+    o *= f;
+    l = fmaf(f, l, g);
+    if (g != 0.f) o = fmaf(g, A.prefix_out[((long long)r * A.nq + j) * D + d], o);
+  }
+  const float y = l != 0.f ? o / l : 0.f;
+  const long long at = r * A.o_row + j * A.o_head + d;
+  if (A.q_f16) reinterpret_cast<__half*>(A.out)[at] = __float2half_rn(y);
+  else reinterpret_cast<bf16*>(A.out)[at] = __float2bfloat16_rn(y);
+}
+
+// Join the pieces of the job that begins in block blockIdx.x: one CTA per (block, row of the
+// tile), its eight warps taking pieces in turn, then summed in warp order.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendArgs A) {
+  __shared__ float so[8][D], sm[8], sl[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 note = A.notes[2 * c0];
+  const int b = note.x, h = note.y, tile = note.z, parts = note.w;
+  if (tile < 0) return;
+  const int row = tile * ROWS + blockIdx.y;
+  const int row0 = A.a.starts[b], R = (A.a.starts[b + 1] - row0) * A.G;
+  if (row >= R) return;
+  const int4 note2 = A.notes[2 * c0 + 1];
+  const long long total = (long long)(uint32_t)note2.x | ((long long)note2.y << 32);
+  const long long end = (long long)(uint32_t)note2.z | ((long long)note2.w << 32);
+  constexpr int REC = D + 4, V = D / 32;
+  float o[V], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+  for (int c = c0 + warp; c < parts && (c == c0 || cs::range_start(total, parts, c) < end); c += 8) {
+    const float* p = A.pieces + ((2ll * c + (c == c0 ? 1 : 0)) * ROWS + blockIdx.y) * REC;
+    const float pm = p[D], pl = p[D + 1], top = fmaxf(m, pm);
+    const float f = l == 0.f ? 0.f : cs::ex2(m - top), g = pl == 0.f ? 0.f : cs::ex2(pm - top);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = fmaf(g, p[lane * V + i], f * o[i]);
+    l = fmaf(g, pl, f * l);
+    m = top;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) so[warp][lane * V + i] = o[i];
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= D) return;
+  float top = -INFINITY, y = 0.f, sum = 0.f;
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, sm[w]);
+  for (int w = 0; w < 8; ++w) {
+    const float f = sl[w] == 0.f ? 0.f : cs::ex2(sm[w] - top);
+    y = fmaf(f, so[w][d], y);
+    sum = fmaf(f, sl[w], sum);
+  }
+  store_out(A, D, row0 + row / A.G, h * A.G + row % A.G, d, y, sum, top);
+}
+
+}  // namespace jolt

@@ -13,9 +13,9 @@ LIB = os.path.join(HERE, "libjolt.so")
 SOURCES = ["jolt_api.cu", "cache_api.cu"]
 DEPS = ["jolt_api.cu", "common.cuh", "gemm.cuh", "kernels.cuh", "misc.cuh", "umma.cuh", "eig_cluster.cuh", "chol.cuh",
         "fp16_exact.cuh", "table_tc.cuh", "attend.cuh", "eig_large.cuh", "host.cuh", "cache_api.cu", "cache.cuh", "cache_split.cuh",
-        "cache_attend.cuh"]
+        "cache_attend.cuh", "cache_attend_tc.cuh"]
 # the headers each cache source reaches; every other source is rebuilt when anything but these changes
-CACHE = {"cache_api.cu", "cache.cuh", "cache_split.cuh", "cache_attend.cuh"}
+CACHE = {"cache_api.cu", "cache.cuh", "cache_split.cuh", "cache_attend.cuh", "cache_attend_tc.cuh"}
 
 
 def nvcc_cmd(source: str, out: str, extra=()) -> list:

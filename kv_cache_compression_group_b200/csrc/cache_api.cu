@@ -6,6 +6,7 @@
 #include "host.cuh"
 #include "cache.cuh"
 #include "cache_attend.cuh"
+#include "cache_attend_tc.cuh"
 
 using namespace jolt;
 
@@ -89,6 +90,8 @@ jolt_status launch_read(const CacheArgs& c, const BatchArgs& a, const RowsArgs<T
 // rows of one KV head that the narrow kernel takes; more go to the other one
 constexpr int FEW_ROWS = 32;
 
+constexpr int MANY_BLOCKS = 148;   // of the tensor-core kernel: one per SM
+
 // n-tiles of the narrow kernel for at most `rows` rows of a KV head
 int few_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
@@ -110,12 +113,12 @@ struct Scratch {
 };
 Scratch attend_scratch(const CacheArgs& c, const BatchArgs& a, int nq) {
   const long long rows = (long long)a.max_new * (nq / c.H);
-  Scratch s{0, 0, 256};
-  if (rows > FEW_ROWS) return s;
+  const int nt = few_tiles(rows);
+  const size_t blocks = rows > FEW_ROWS ? MANY_BLOCKS : few_blocks(c, nt), tile = rows > FEW_ROWS ? ct::ROWS : 8 * nt;
+  Scratch s;
   Bump m;
-  const int nt = few_tiles(rows), blocks = few_blocks(c, nt);
   s.notes = m.take(sizeof(int4) * 2 * blocks);
-  s.pieces = m.take(sizeof(float) * 2 * blocks * 8 * nt * (c.D + 4));
+  s.pieces = m.take(sizeof(float) * 2 * blocks * tile * (c.D + 4));
   s.total = m.off;
   return s;
 }
@@ -143,7 +146,7 @@ jolt_status launch_few(const CacheAttendArgs& A, cudaStream_t st) {
   CUDA_TRY(cudaFuncSetAttribute(cache_few_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   count_launch(), cache_few_rows_kernel<D, NT><<<blocks, ca::WARPS * 32, smem, st>>>(A);
   CUDA_TRY(cudaGetLastError());
-  CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT>, dim3(blocks, A.a.max_new * A.G), 256, A, st));
+  CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT, 8>, dim3(blocks, A.a.max_new * A.G), 256, A, st));
   return JOLT_OK;
 }
 
@@ -157,8 +160,11 @@ jolt_status launch_cache_attend(const CacheAttendArgs& A, cudaStream_t st) {
       default: return launch_few<D, 4>(A, st);
     }
   }
-  count_launch(), cache_attend_kernel<D><<<dim3(A.a.rows, A.nq), D, 0, st>>>(A);
+  constexpr int smem = ct::Smem<D>::BYTES;
+  CUDA_TRY(cudaFuncSetAttribute(cache_many_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  count_launch(), cache_many_rows_kernel<D><<<MANY_BLOCKS, ct::THREADS, smem, st>>>(A);
   CUDA_TRY(cudaGetLastError());
+  CUDA_TRY(launch_after(cache_join_kernel<D, ct::ROWS, 1>, dim3(MANY_BLOCKS, ct::ROWS / 8), 256, A, st));
   return JOLT_OK;
 }
 
@@ -259,6 +265,7 @@ jolt_status jolt_cache_attend(const jolt_cache* cache, const jolt_cache_batch* b
   A.q_f16 = dtype == JOLT_F16;
   A.q_row = q_row_stride;
   A.q_head = q_head_stride;
+  A.q_vec = aligned16(q_dev) && q_row_stride % 8 == 0 && q_head_stride % 8 == 0;
   A.out = out_dev;
   A.o_row = out_row_stride;
   A.o_head = out_head_stride;

@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
   long long base = s_base;
   const bool plain = A.cap == 0.f;
 
-  while (w < w1) {
+  while (w < w1 && b < A.a.B) {
     const int units = cache_units(A, b, UNIT, row0, n, len, first);
     if (w >= base + (long long)units * A.c.H) {   // next sequence (those without units are passed over)
       base += (long long)units * A.c.H;
@@ -588,69 +588,6 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     }
     w += u1 - u0;
   }
-}
-
-// ---- the plain kernel for more rows --------------------------------------------------------
-__device__ __forceinline__ float cache_value(const CacheArgs& c, int kv, long long row, int d) {
-  const int b = c.bits[kv], nb = c.D / pc::BLK, bit = d * b;
-  const long long at = row * nb;
-  const uint32_t byte = c.codes[kv][at * (2 * b) + (bit >> 3)];
-  const float2 s = __half22float2(c.scales[kv][at + d / pc::BLK]);
-  return fmaf((float)((byte >> (bit & 7)) & ((1u << b) - 1u)), s.y, s.x);
-}
-
-// One CTA of D threads per (new row, query head): tiles of D keys, one key per thread for the
-// scores, one feature per thread for the values.
-template <int D>
-__global__ void __launch_bounds__(D) cache_attend_kernel(CacheAttendArgs A) {
-  __shared__ float qs[D], ps[D], red[D / 32];
-  __shared__ long long rowof[D];
-  const int r = blockIdx.x, j = blockIdx.y, h = j / A.G, tid = threadIdx.x;
-  const int b = seq_of_row(A.a, r);
-  int row0, n, len;
-  if (b < 0 || !seq_of(A.a, A.c.page_shift, b, row0, n, len)) return;
-  const int i = r - row0, old = len - n;
-  qs[tid] = ld_q(A, r * A.q_row + j * A.q_head + tid);
-  const int pq = A.positions ? A.positions[r] : old + i;
-  const float slope = A.slopes ? A.slopes[j] * cs::LOG2E : 0.f;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  const int first = A.window ? max(0, old - A.window + 1) : 0;
-  __syncthreads();
-  for (int t0 = first; t0 < len; t0 += D) {
-    const int t = t0 + tid;
-    float s = -INFINITY;
-    rowof[tid] = -1;
-    if (t < len) {
-      const int page = page_at(A.a, A.c, b, t), pk = key_position(A, row0, old, t);
-      if (page >= 0 && row_sees(A, row0, old, n, i, pq, t, pk)) {
-        const long long row = row_index(A.c, page, h, t);
-        rowof[tid] = row;
-        s = 0.f;
-        for (int d = 0; d < D; ++d) s = fmaf(qs[d], cache_value(A.c, 0, row, d), s);
-        s *= A.scale;
-        if (A.cap > 0.f) s = cap_score(s, A.cap);
-        s = fmaf(-slope, (float)(pq - pk), s * cs::LOG2E);
-      }
-    }
-    float mx = s;
-    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    for (int k = 0; k < D / 32; ++k) mx = fmaxf(mx, red[k]);
-    const float mn = fmaxf(m, mx), f = m == -INFINITY ? 0.f : cs::ex2(m - mn);
-    ps[tid] = s == -INFINITY ? 0.f : cs::ex2(s - mn + cs::SHIFT);
-    m = mn;
-    __syncthreads();
-    l *= f;
-    o *= f;
-    for (int k = 0; k < D; ++k)
-      if (rowof[k] >= 0) {
-        l += ps[k];
-        o = fmaf(ps[k], cache_value(A.c, 1, rowof[k], tid), o);
-      }
-    __syncthreads();
-  }
-  store_out(A, D, r, j, tid, o, l, m);
 }
 
 }  // namespace jolt

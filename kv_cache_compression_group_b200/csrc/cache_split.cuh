@@ -31,6 +31,7 @@ struct CacheAttendArgs {
   long long q_row, q_head;
   void* out;
   long long o_row, o_head;
+  bool q_vec;                // rows and heads of q are 16-byte aligned
   // scratch
   int4* notes;               // [blocks][2]: {sequence, KV head, row tile or -1, -}, {units in all, end of the job}
   float* pieces;             // [blocks][2][rows of a tile][D + 4]: D outputs, maximum, sum
@@ -99,9 +100,10 @@ __device__ __forceinline__ void store_out(const CacheAttendArgs& A, int D, int r
   else reinterpret_cast<bf16*>(A.out)[at] = __float2bfloat16_rn(y);
 }
 
-// Join the pieces of the job that begins in block blockIdx.x: one CTA per (block, row of the
-// tile), its eight warps taking pieces in turn, then summed in warp order.
-template <int D, int ROWS>
+// Join the pieces of the job that begins in block blockIdx.x, 8 / SPLIT rows of its tile per CTA:
+// SPLIT of the eight warps take a row's pieces in turn, and their sums are added in warp order.
+// (A few rows of few jobs have up to 74 pieces each; 128 rows of many jobs mostly two.)
+template <int D, int ROWS, int SPLIT>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendArgs A) {
   __shared__ float so[8][D], sm[8], sl[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -109,9 +111,9 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendArgs A) {
   const int4 note = A.notes[2 * c0];
   const int b = note.x, h = note.y, tile = note.z, parts = note.w;
   if (tile < 0) return;
-  const int row = tile * ROWS + blockIdx.y;
+  const int mine = blockIdx.y * (8 / SPLIT) + warp / SPLIT;   // row of the tile
+  const int row = tile * ROWS + mine;
   const int row0 = A.a.starts[b], R = (A.a.starts[b + 1] - row0) * A.G;
-  if (row >= R) return;
   const int4 note2 = A.notes[2 * c0 + 1];
   const long long total = (long long)(uint32_t)note2.x | ((long long)note2.y << 32);
   const long long end = (long long)(uint32_t)note2.z | ((long long)note2.w << 32);
@@ -119,8 +121,9 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendArgs A) {
   float o[V], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.f;
-  for (int c = c0 + warp; c < parts && (c == c0 || cs::range_start(total, parts, c) < end); c += 8) {
-    const float* p = A.pieces + ((2ll * c + (c == c0 ? 1 : 0)) * ROWS + blockIdx.y) * REC;
+  for (int c = c0 + warp % SPLIT; row < R && c < parts && (c == c0 || cs::range_start(total, parts, c) < end);
+       c += SPLIT) {
+    const float* p = A.pieces + ((2ll * c + (c == c0 ? 1 : 0)) * ROWS + mine) * REC;
     const float pm = p[D], pl = p[D + 1], top = fmaxf(m, pm);
     const float f = l == 0.f ? 0.f : cs::ex2(m - top), g = pl == 0.f ? 0.f : cs::ex2(pm - top);
 #pragma unroll
@@ -135,16 +138,18 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendArgs A) {
     sl[warp] = l;
   }
   __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= D) return;
-  float top = -INFINITY, y = 0.f, sum = 0.f;
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, sm[w]);
-  for (int w = 0; w < 8; ++w) {
-    const float f = sl[w] == 0.f ? 0.f : cs::ex2(sm[w] - top);
-    y = fmaf(f, so[w][d], y);
-    sum = fmaf(f, sl[w], sum);
+  for (int idx = threadIdx.x; idx < 8 / SPLIT * D; idx += 256) {
+    const int first = idx / D * SPLIT, d = idx % D, out = tile * ROWS + blockIdx.y * (8 / SPLIT) + idx / D;
+    if (out >= R) break;
+    float top = -INFINITY, y = 0.f, sum = 0.f;
+    for (int w = first; w < first + SPLIT; ++w) top = fmaxf(top, sm[w]);
+    for (int w = first; w < first + SPLIT; ++w) {
+      const float f = sl[w] == 0.f ? 0.f : cs::ex2(sm[w] - top);
+      y = fmaf(f, so[w][d], y);
+      sum = fmaf(f, sl[w], sum);
+    }
+    store_out(A, D, row0 + out / A.G, h * A.G + out % A.G, d, y, sum, top);
   }
-  store_out(A, D, row0 + row / A.G, h * A.G + row % A.G, d, y, sum, top);
 }
 
 }  // namespace jolt

@@ -124,7 +124,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) { retur
 // on it only if `arrive` is set, and waits for phase 0 with the given limit.  Without the
 // arrival the phase never completes, the wait gives up and DEV_ERR_TIMEOUT is raised; the
 // kernel then returns normally.
-__global__ void wait_selftest_kernel(int arrive, uint64_t limit_ns, uint32_t* status) {
+static __global__ void wait_selftest_kernel(int arrive, uint64_t limit_ns, uint32_t* status) {
   __shared__ __align__(8) uint64_t bar;
   if (threadIdx.x != 0) return;
   const uint32_t b = smem_u32(&bar);

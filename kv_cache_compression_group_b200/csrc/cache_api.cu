@@ -5,7 +5,7 @@
 #include "common.cuh"
 #include "host.cuh"
 #include "cache.cuh"
-#include "cache_attend.cuh"
+#include "cache_launch.cuh"
 #include "cache_attend_tc.cuh"
 
 using namespace jolt;
@@ -87,27 +87,6 @@ jolt_status launch_read(const CacheArgs& c, const BatchArgs& a, const RowsArgs<T
   return JOLT_OK;
 }
 
-// rows of one KV head that the narrow kernel takes; more go to the other one
-constexpr int FEW_ROWS = 32;
-
-constexpr int MANY_BLOCKS = 148;   // of the tensor-core kernel: one per SM
-
-// n-tiles of the narrow kernel for at most `rows` rows of a KV head
-int few_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
-
-// shared memory of the narrow kernel, and its blocks: as many as the GPU holds at once (by
-// registers 4, 3 or 2 per SM, by shared memory what 228 KB hold with 1 KB reserved for each)
-int few_smem(const CacheArgs& c, int nt) {
-  const int bk = c.bits[0], bv = c.bits[1];
-  if (c.D == 64)
-    return nt == 1 ? ca::Smem<64, 1>::bytes(bk, bv) : nt == 2 ? ca::Smem<64, 2>::bytes(bk, bv) : ca::Smem<64, 4>::bytes(bk, bv);
-  return nt == 1 ? ca::Smem<128, 1>::bytes(bk, bv) : nt == 2 ? ca::Smem<128, 2>::bytes(bk, bv) : ca::Smem<128, 4>::bytes(bk, bv);
-}
-int few_blocks(const CacheArgs& c, int nt) {
-  const int by_regs = nt == 1 ? 4 : nt == 2 ? 3 : 2, by_smem = 228 * 1024 / (few_smem(c, nt) + 1024);
-  return 148 * (by_regs < by_smem ? by_regs : by_smem);
-}
-
 struct Scratch {
   size_t notes, pieces, total;
 };
@@ -117,54 +96,21 @@ Scratch attend_scratch(const CacheArgs& c, const BatchArgs& a, int nq) {
   const size_t blocks = rows > FEW_ROWS ? MANY_BLOCKS : few_blocks(c, nt), tile = rows > FEW_ROWS ? ct::ROWS : 8 * nt;
   Scratch s;
   Bump m;
-  s.notes = m.take(sizeof(int4) * 2 * blocks);
+  s.notes = m.take(sizeof(int4) * blocks);
   s.pieces = m.take(sizeof(float) * 2 * blocks * tile * (c.D + 4));
   s.total = m.off;
   return s;
 }
 
-// launch with programmatic stream serialization: the join's blocks may be scheduled while the
-// last blocks of the kernel before it run; they wait for its end before they read
-template <typename K>
-cudaError_t launch_after(K kernel, dim3 grid, int threads, const CacheAttendArgs& A, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  count_launch();
-  return cudaLaunchKernelEx(&cfg, kernel, A);
-}
-
-template <int D, int NT>
-jolt_status launch_few(const CacheAttendArgs& A, cudaStream_t st) {
-  const int smem = few_smem(A.c, NT), blocks = few_blocks(A.c, NT);
-  CUDA_TRY(cudaFuncSetAttribute(cache_few_rows_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  count_launch(), cache_few_rows_kernel<D, NT><<<blocks, ca::WARPS * 32, smem, st>>>(A);
-  CUDA_TRY(cudaGetLastError());
-  CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT, 8>, dim3(blocks, A.a.max_new * A.G), 256, A, st));
-  return JOLT_OK;
-}
-
 template <int D>
 jolt_status launch_cache_attend(const CacheAttendArgs& A, cudaStream_t st) {
   const long long rows = (long long)A.a.max_new * A.G;
-  if (rows <= FEW_ROWS) {
-    switch (few_tiles(rows)) {
-      case 1: return launch_few<D, 1>(A, st);
-      case 2: return launch_few<D, 2>(A, st);
-      default: return launch_few<D, 4>(A, st);
-    }
-  }
+  if (rows <= FEW_ROWS) return launch_few_rows<D>(A, few_tiles(rows), st);
   constexpr int smem = ct::Smem<D>::BYTES;
   CUDA_TRY(cudaFuncSetAttribute(cache_many_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   count_launch(), cache_many_rows_kernel<D><<<MANY_BLOCKS, ct::THREADS, smem, st>>>(A);
   CUDA_TRY(cudaGetLastError());
-  CUDA_TRY(launch_after(cache_join_kernel<D, ct::ROWS, 1>, dim3(MANY_BLOCKS, ct::ROWS / 8), 256, A, st));
+  CUDA_TRY(launch_after(cache_join_kernel<D, ct::ROWS, 8, 1>, dim3(MANY_BLOCKS, ct::ROWS / 8), 256, A, st));
   return JOLT_OK;
 }
 

@@ -61,25 +61,38 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ uint32_t h2u(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ __half2 u2h(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
+// The exponent of 1024 in both halves, in a register the compiler cannot see through: with it, mask
+// and exponent go in by one three-input logic operation (as two immediates they would take two).
+__device__ __forceinline__ uint32_t magic1024() {
+  uint32_t x;
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(x));
+  return x;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t magic) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(a), "r"(mask), "r"(magic));
+  return y;
+}
+
 // Codes s of the two 16-bit halves of w as an fp16 pair: the code under the exponent of 1024
-// (or of 1024 with the code 16 times too large, for a nibble that is not shifted down), made exact
-// by one subtraction (or fused multiply-add).
+// (or of 1024 with the code 4^k times too large, where it is not shifted down), made exact by one
+// subtraction (or fused multiply-add).
 template <int BITS>
-__device__ __forceinline__ __half2 code_pair(uint32_t w, int s) {
+__device__ __forceinline__ __half2 code_pair(uint32_t w, int s, uint32_t magic) {
   const __half2 k1024 = __float2half2_rn(-1024.f);
   if constexpr (BITS == 2) {
     const uint32_t v = s < 4 ? w : w >> 8;
     const int p = 2 * (s & 3);
-    const uint32_t x = (v & (0x00030003u << p)) | 0x64006400u;
+    const uint32_t x = and_or(v, 0x00030003u << p, magic);
     if (p == 0) return __hadd2(u2h(x), k1024);
     const float f = 1.f / (float)(1 << p);
     return __hfma2(u2h(x), __float2half2_rn(f), __float2half2_rn(-1024.f * f));
   } else if constexpr (BITS == 4) {
     const uint32_t v = s < 2 ? w : w >> 8;
-    if ((s & 1) == 0) return __hadd2(u2h((v & 0x000f000fu) | 0x64006400u), k1024);
-    return __hfma2(u2h((v & 0x00f000f0u) | 0x64006400u), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
+    if ((s & 1) == 0) return __hadd2(u2h(and_or(v, 0x000f000fu, magic)), k1024);
+    return __hfma2(u2h(and_or(v, 0x00f000f0u, magic)), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
   } else {
-    return __hadd2(u2h(__byte_perm(w, 0x64646464u, s == 0 ? 0x4240 : 0x4341)), k1024);
+    return __hadd2(u2h(__byte_perm(w, magic, s == 0 ? 0x5250 : 0x5351)), k1024);
   }
 }
 
@@ -90,26 +103,19 @@ __device__ __forceinline__ int swizzled(int row, int ch) {
   return (row * CH + (CH == 1 ? ch : ch ^ ((row / (8 / CH)) & (CH - 1)))) * 16;
 }
 
-// copy a stage's rows (16 x CH chunks, contiguous in the page) to shared memory
+// Copy a stage's rows (16 x CH chunks, contiguous in the page) to shared memory.  dst0: where this
+// lane's first chunk goes, swizzled<CH>(lane / CH, lane % CH); its next ones follow 512 bytes apart
+// (with CH = 8 every other one in the other half of its row).
 template <int CH>
-__device__ __forceinline__ void copy_rows(uint32_t dst, const unsigned char* src, int lane) {
+__device__ __forceinline__ void copy_rows(uint32_t stage, uint32_t dst0, const unsigned char* src, int lane) {
 #pragma unroll
-  for (int i = 0; i < (CH + 1) / 2; ++i) {
-    const int idx = lane + 32 * i;
-    if (CH > 1 || lane < 16) cp16(dst + swizzled<CH>(idx / CH, idx % CH), src + 16 * idx);
-  }
-}
-
-template <int D>
-__device__ __forceinline__ void copy_codes(uint32_t dst, const unsigned char* src, int bits, int lane) {
-  if (bits == 4) copy_rows<D / 32>(dst, src, lane);
-  else if (bits == 8) copy_rows<D / 16>(dst, src, lane);
-  else copy_rows<D / 64>(dst, src, lane);
+  for (int i = 0; i < (CH + 1) / 2; ++i)
+    if (CH > 1 || lane < 16) cp16(stage + (CH == 8 && (i & 1) ? dst0 ^ 64u : dst0) + 512 * i, src + 512 * i);
 }
 
 // S^T += K Q^T for 16 tokens; q(m, nt) gives B registers of product m and n-tile nt
 template <int BITS, int D, int NT, typename QF>
-__device__ __forceinline__ void scores(float (&s)[NT][4], uint32_t kc, const unsigned char* ksc, int lane, QF&& q) {
+__device__ __forceinline__ void scores(float (&s)[NT][4], uint32_t kc, uint32_t ksc, int lane, uint32_t magic, QF&& q) {
   constexpr int CH = D * BITS / 128, W = D / 4 * BITS / 32;   // chunks per row, words per thread and token
   const int g = lane >> 2, c = lane & 3;
   uint32_t w[2][W];
@@ -133,11 +139,17 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], uint32_t kc, const uns
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[t][0]) : "r"(kc + row * 16 + c * 4) : "memory");
     }
     if constexpr (D == 128) {
-      const uint2 v = *reinterpret_cast<const uint2*>(ksc + swizzled<2>(row, c >> 1) + (c & 1) * 8);
+      uint2 v;
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                   : "=r"(v.x), "=r"(v.y)
+                   : "r"(ksc + swizzled<2>(row, c >> 1) + (c & 1) * 8)
+                   : "memory");
       sc[t][0] = u2h(v.x);
       sc[t][1] = u2h(v.y);
     } else {
-      sc[t][0] = u2h(*reinterpret_cast<const uint32_t*>(ksc + row * 16 + c * 4));
+      uint32_t v;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(ksc + row * 16 + c * 4) : "memory");
+      sc[t][0] = u2h(v);
     }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) sc[t][i] = __hmul2(sc[t][i], __float2half2_rn(0.5f));
@@ -151,7 +163,7 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], uint32_t kc, const uns
     for (int t = 0; t < 2; ++t) {
       const __half2 lo = __low2half2(sc[t][blk]), step = __high2half2(sc[t][blk]);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) a[t][r] = h2u(__hfma2(code_pair<BITS>(w[t][word], pair + r), step, lo));
+      for (int r = 0; r < 2; ++r) a[t][r] = h2u(__hfma2(code_pair<BITS>(w[t][word], pair + r, magic), step, lo));
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -165,7 +177,7 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], uint32_t kc, const uns
 // (2c + 8, 2c + 9), zero where a token lies behind the sequence
 template <int BITS, int D, int NT>
 __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], uint32_t vc, uint32_t vsc, int lane,
-                                       const uint32_t (&p)[NT][2], uint32_t live0, uint32_t live1) {
+                                       const uint32_t (&p)[NT][2], uint32_t live0, uint32_t live1, uint32_t magic) {
   constexpr int CH = D * BITS / 128, CPU = 16 / BITS, SCH = D / 64;
   const int g = lane >> 2, c = lane & 3;
   // (lo, step) of the row's blocks: column 2 blk + {0, 1}, rows = tokens
@@ -201,10 +213,10 @@ __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], uint32_t vc, u
       const __half2 st1 = u2h(__shfl_sync(0xffffffffu, sc[2 * z + 1], src + 4));
 #pragma unroll
       for (int sp = 0; sp < CPU / 2; ++sp) {
-        const uint32_t a0 = h2u(__hfma2(code_pair<BITS>(r[2 * u], 2 * sp), st0, lo0));
-        const uint32_t a1 = h2u(__hfma2(code_pair<BITS>(r[2 * u], 2 * sp + 1), st0, lo0));
-        const uint32_t a2 = h2u(__hfma2(code_pair<BITS>(r[2 * u + 1], 2 * sp), st1, lo1));
-        const uint32_t a3 = h2u(__hfma2(code_pair<BITS>(r[2 * u + 1], 2 * sp + 1), st1, lo1));
+        const uint32_t a0 = h2u(__hfma2(code_pair<BITS>(r[2 * u], 2 * sp, magic), st0, lo0));
+        const uint32_t a1 = h2u(__hfma2(code_pair<BITS>(r[2 * u], 2 * sp + 1, magic), st0, lo0));
+        const uint32_t a2 = h2u(__hfma2(code_pair<BITS>(r[2 * u + 1], 2 * sp, magic), st1, lo1));
+        const uint32_t a3 = h2u(__hfma2(code_pair<BITS>(r[2 * u + 1], 2 * sp + 1, magic), st1, lo1));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][qc * (CPU / 2) + sp], a0, a1, a2, a3, p[nt][0], p[nt][1]);
       }
@@ -243,7 +255,165 @@ __device__ __forceinline__ int cache_units(const CacheAttendArgs& A, int b, int 
   return (len - first + unit - 1) / unit;
 }
 
-template <int D, int NT>
+// What a warp needs of its job; the arrays are the kernel's registers.
+template <int NT>
+struct FewJob {
+  int b, h, row0, n, len;
+  int tw, count;           // first token of the warp's first stage; stages, UNIT tokens apart
+  int edge, R;             // keys from `edge` on are inside every row's window; rows
+  const float (&mult)[NT][2];
+  const float (&slope)[NT][2];
+  const int (&pq)[NT][2];
+};
+
+// A warp's stages, each of 16 tokens: copies run stages() - 1 ahead of the products.
+template <int D, int NT, int KB, int VB, typename QF>
+__device__ __forceinline__ void few_loop(const CacheAttendArgs& A, const FewJob<NT>& J, unsigned char* mine, int lane,
+                                         QF&& q_of, float (&o)[NT][D / 16][4], float (&m_ref)[NT][2],
+                                         float (&l)[NT][2]) {
+  using namespace ca;
+  constexpr int NST = stages(D, KB, VB), KBYTES = TOK * D * KB / 8, VBYTES = TOK * D * VB / 8, SBYTES = TOK * D / 4;
+  constexpr int STAGE = KBYTES + VBYTES + 2 * SBYTES, KCH = D * KB / 128, VCH = D * VB / 128, SCH = D / 64;
+  const int g = lane >> 2, c = lane & 3, len = J.len, old = J.len - J.n, count = J.count, tw = J.tw;
+  const bool plain = A.cap == 0.f;
+  const uint32_t magic = magic1024(), ring = smem_addr(mine);
+  const uint32_t kdst = swizzled<KCH>(lane / KCH, lane % KCH), vdst = KBYTES + SBYTES + swizzled<VCH>(lane / VCH, lane % VCH);
+  const uint32_t ksd = KBYTES + swizzled<SCH>(lane / SCH, lane % SCH), vsd = ksd + SBYTES + VBYTES;
+  const unsigned char* kc = A.c.codes[0] + lane * 16;
+  const unsigned char* vc = A.c.codes[1] + lane * 16;
+  const unsigned char* ks = reinterpret_cast<const unsigned char*>(A.c.scales[0]) + lane * 16;
+  const unsigned char* vs = reinterpret_cast<const unsigned char*>(A.c.scales[1]) + lane * 16;
+  const int* table = A.a.table + (long long)J.b * A.a.max_pages;
+  // a stage's page is looked up one stage ahead of its copies
+  int t_issue = tw, left = count;        // token of the next stage to copy; how many are to copy
+  int page = left > 0 ? table[t_issue >> A.c.page_shift] : 0;
+  uint32_t st_issue = 0;                 // its place in the ring
+  unsigned lost = 0;                     // bit k: the stage k after the one in work has no page
+  auto issue = [&](int ahead) {
+    if (left > 0) {
+      const int mine_page = page, t = t_issue;
+      --left;
+      t_issue += UNIT;
+      if (left > 0) page = table[t_issue >> A.c.page_shift];
+      if ((unsigned)mine_page < (unsigned)A.c.n_pages) {
+        const long long row = row_index(A.c, mine_page, J.h, t);
+        const uint32_t dst = ring + st_issue;
+        copy_rows<KCH>(dst, kdst, kc + row * (D * KB / 8), lane);
+        copy_rows<SCH>(dst, ksd, ks + row * (D / 4), lane);
+        copy_rows<VCH>(dst, vdst, vc + row * (D * VB / 8), lane);
+        copy_rows<SCH>(dst, vsd, vs + row * (D / 4), lane);
+      } else {
+        lost |= 1u << ahead;
+        raise_status(A.a.status, DEV_ERR_BATCH);
+      }
+      st_issue = st_issue == (NST - 1) * STAGE ? 0 : st_issue + STAGE;
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) issue(i);
+  uint32_t st = ring;
+  for (int i = 0, t0 = tw; i < count; ++i, t0 += UNIT) {
+    cp_wait<NST - 2>();
+    __syncwarp();                        // everyone's copies of this stage are here, and the one before is read
+    issue(NST - 1);
+    const bool skip = lost & 1u;
+    lost >>= 1;
+    const uint32_t sta = st;
+    st = st == ring + (NST - 1) * STAGE ? ring : st + STAGE;
+    if (skip) continue;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[nt][k] = 0.f;
+    scores<KB, D, NT>(s, sta, sta + KBYTES, lane, magic, q_of);
+    // ---- scores to base 2: s[nt][2 t + k] is token g + 8 t, row 8 nt + 2 c + k ----
+    const bool ragged = t0 + TOK > old || t0 < J.edge;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[nt][k] *= J.mult[nt][k & 1];
+    if (!plain) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[nt][k] = cap_score(s[nt][k], A.cap) * cs::LOG2E;
+    }
+    if (ragged) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int t = t0 + g + 8 * (k >> 1);
+        const int pk = t < len ? key_position(A, J.row0, old, t) : 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = 8 * nt + 2 * c + (k & 1);
+          const bool sees = t < len && r < J.R && row_sees(A, J.row0, old, J.n, r / A.G, J.pq[nt][k & 1], t, pk);
+          s[nt][k] = sees ? fmaf(-J.slope[nt][k & 1], (float)(J.pq[nt][k & 1] - pk), s[nt][k]) : -INFINITY;
+        }
+      }
+    } else if (A.slopes) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          s[nt][k] = fmaf(-J.slope[nt][k & 1], (float)(J.pq[nt][k & 1] - (t0 + g + 8 * (k >> 1))), s[nt][k]);
+    }
+    // ---- running softmax over the tokens ----
+    bool grow = false;
+    float mx[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        mx[nt][k] = fmaxf(s[nt][k], s[nt][2 + k]);
+        grow |= mx[nt][k] > m_ref[nt][k] + cs::LAG;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float x = mx[nt][k];
+#pragma unroll
+          for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
+          const float to = fmaxf(x, m_ref[nt][k]);
+          const float f = m_ref[nt][k] == -INFINITY ? 0.f : cs::ex2(m_ref[nt][k] - to);
+          m_ref[nt][k] = to;
+          l[nt][k] *= f;
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            o[nt][mt][k] *= f;
+            o[nt][mt][2 + k] *= f;
+          }
+        }
+      }
+    }
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float e[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float ref = m_ref[nt][k & 1] == -INFINITY ? 0.f : m_ref[nt][k & 1] - cs::SHIFT;
+        e[k] = cs::ex2(s[nt][k] - ref);
+        l[nt][k & 1] += e[k];
+      }
+      p[nt][0] = transpose8(h2u(__floats2half2_rn(e[0], e[1])));
+      p[nt][1] = transpose8(h2u(__floats2half2_rn(e[2], e[3])));
+    }
+    uint32_t live0 = 0xffffffffu, live1 = 0xffffffffu;
+    if (t0 + TOK > len) {
+      const int t = t0 + 2 * c;
+      live0 = (t < len ? 0xffffu : 0u) | (t + 1 < len ? 0xffff0000u : 0u);
+      live1 = (t + 8 < len ? 0xffffu : 0u) | (t + 9 < len ? 0xffff0000u : 0u);
+    }
+    values<VB, D, NT>(o, sta + KBYTES + SBYTES, sta + KBYTES + SBYTES + VBYTES, lane, p, live0, live1, magic);
+  }
+  cp_wait<0>();
+}
+
+template <int D, int NT, int KB, int VB>
 __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2) cache_few_rows_kernel(CacheAttendArgs A) {
   using namespace ca;
   using S = Smem<D, NT>;
@@ -255,9 +425,8 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
   __shared__ long long s_sum[WARPS], s_base;
   __shared__ int s_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int bk = A.c.bits[0], bv = A.c.bits[1];
-  const int nst = stages(D, bk, bv), kbytes = TOK * D * bk / 8, vbytes = TOK * D * bv / 8, sbytes = TOK * D / 4;
-  unsigned char* mine = ring + warp * nst * stage_bytes(D, bk, bv);
+  constexpr int bk = KB, bv = VB;
+  unsigned char* mine = ring + warp * stages(D, bk, bv) * stage_bytes(D, bk, bv);
   int row0, n, len, first;
 
   // ---- this block's range of units: all units, then the sequence in which the range begins ----
@@ -267,7 +436,7 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
   if (lane == 0) s_sum[warp] = total;
-  if (tid == 0) A.notes[2 * blockIdx.x] = make_int4(0, 0, -1, 0);
+  if (tid == 0) A.notes[blockIdx.x] = make_int4(0, 0, -1, 0);
   __syncthreads();
   total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
   const int parts = (int)min((long long)gridDim.x, total);
@@ -396,142 +565,13 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
         for (int k = 0; k < 4; ++k) o[nt][mt][k] = 0.f;
     }
 
-    // ---- this warp's stages: tokens t_of(i) .. + 15 of unit u0 + i ----
+    // ---- this warp's share of the keys ----
     const int tw = first + u0 * UNIT + warp * TOK;
     int count = u1 - u0;
     if (tw + (count - 1) * UNIT >= len) count = tw < len ? (len - 1 - tw) / UNIT + 1 : 0;
-    // a stage's page is looked up one stage ahead of its copies
-    const int* table = A.a.table + (long long)b * A.a.max_pages;
-    auto page_of = [&](int i) { return i < count ? table[(tw + i * UNIT) >> A.c.page_shift] : 0; };
-    int page = page_of(0);
-    unsigned lost = 0;                   // bit i % 32: stage i's page does not exist
-    auto issue = [&](int i) {
-      const int mine_page = page;
-      page = page_of(i + 1);
-      if (i < count) {
-        const int t = tw + i * UNIT;
-        const unsigned bit = 1u << (i & 31);
-        if ((unsigned)mine_page < (unsigned)A.c.n_pages) {
-          lost &= ~bit;
-          const long long row = row_index(A.c, mine_page, h, t);
-          const uint32_t dst = smem_addr(mine + (i % nst) * stage_bytes(D, bk, bv));
-          copy_codes<D>(dst, A.c.codes[0] + row * (D * bk / 8), bk, lane);
-          copy_rows<D / 64>(dst + kbytes, reinterpret_cast<const unsigned char*>(A.c.scales[0] + row * (D / 16)), lane);
-          copy_codes<D>(dst + kbytes + sbytes, A.c.codes[1] + row * (D * bv / 8), bv, lane);
-          copy_rows<D / 64>(dst + kbytes + sbytes + vbytes,
-                            reinterpret_cast<const unsigned char*>(A.c.scales[1] + row * (D / 16)), lane);
-        } else {
-          lost |= bit;
-          raise_status(A.a.status, DEV_ERR_BATCH);
-        }
-      }
-      cp_commit();
-    };
-    for (int i = 0; i < nst - 1; ++i) issue(i);
-    for (int i = 0; i < count; ++i) {
-      if (nst == 3) cp_wait<1>();
-      else cp_wait<2>();
-      __syncwarp();                      // everyone's copies of stage i are here, and stage i - 1 is read
-      issue(i + nst - 1);
-      if ((lost >> (i & 31)) & 1u) continue;
-      const int t0 = tw + i * UNIT;
-      unsigned char* st = mine + (i % nst) * stage_bytes(D, bk, bv);
-      const uint32_t sta = smem_addr(st);
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[nt][k] = 0.f;
-      if (bk == 4) scores<4, D, NT>(s, sta, st + kbytes, lane, q_of);
-      else if (bk == 8) scores<8, D, NT>(s, sta, st + kbytes, lane, q_of);
-      else scores<2, D, NT>(s, sta, st + kbytes, lane, q_of);
-      // ---- scores to base 2: s[nt][2 t + k] is token g + 8 t, row 8 nt + 2 c + k ----
-      const bool ragged = t0 + TOK > old || t0 < edge;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[nt][k] *= mult[nt][k & 1];
-      if (!plain) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[nt][k] = cap_score(s[nt][k], A.cap) * cs::LOG2E;
-      }
-      if (ragged) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int t = t0 + g + 8 * (k >> 1);
-          const int pk = t < len ? key_position(A, row0, old, t) : 0;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const int r = 8 * nt + 2 * c + (k & 1);
-            const bool sees = t < len && r < R && row_sees(A, row0, old, n, r / A.G, pq[nt][k & 1], t, pk);
-            s[nt][k] = sees ? fmaf(-slope[nt][k & 1], (float)(pq[nt][k & 1] - pk), s[nt][k]) : -INFINITY;
-          }
-        }
-      } else if (A.slopes) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            s[nt][k] = fmaf(-slope[nt][k & 1], (float)(pq[nt][k & 1] - (t0 + g + 8 * (k >> 1))), s[nt][k]);
-      }
-      // ---- running softmax over the tokens ----
-      bool grow = false;
-      float mx[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mx[nt][k] = fmaxf(s[nt][k], s[nt][2 + k]);
-          grow |= mx[nt][k] > m_ref[nt][k] + cs::LAG;
-        }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float x = mx[nt][k];
-#pragma unroll
-            for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
-            const float to = fmaxf(x, m_ref[nt][k]);
-            const float f = m_ref[nt][k] == -INFINITY ? 0.f : cs::ex2(m_ref[nt][k] - to);
-            m_ref[nt][k] = to;
-            l[nt][k] *= f;
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) {
-              o[nt][mt][k] *= f;
-              o[nt][mt][2 + k] *= f;
-            }
-          }
-        }
-      }
-      uint32_t p[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float e[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float ref = m_ref[nt][k & 1] == -INFINITY ? 0.f : m_ref[nt][k & 1] - cs::SHIFT;
-          e[k] = cs::ex2(s[nt][k] - ref);
-          l[nt][k & 1] += e[k];
-        }
-        p[nt][0] = transpose8(h2u(__floats2half2_rn(e[0], e[1])));
-        p[nt][1] = transpose8(h2u(__floats2half2_rn(e[2], e[3])));
-      }
-      uint32_t live0 = 0xffffffffu, live1 = 0xffffffffu;
-      if (t0 + TOK > len) {
-        const int t = t0 + 2 * c;
-        live0 = (t < len ? 0xffffu : 0u) | (t + 1 < len ? 0xffff0000u : 0u);
-        live1 = (t + 8 < len ? 0xffffu : 0u) | (t + 9 < len ? 0xffff0000u : 0u);
-      }
-      const uint32_t vc = sta + kbytes + sbytes, vs = vc + vbytes;
-      if (bv == 4) values<4, D, NT>(o, vc, vs, lane, p, live0, live1);
-      else if (bv == 8) values<8, D, NT>(o, vc, vs, lane, p, live0, live1);
-      else values<2, D, NT>(o, vc, vs, lane, p, live0, live1);
-    }
+    const FewJob<NT> job{b, h, row0, n, len, tw, count, edge, R, mult, slope, pq};
+    few_loop<D, NT, KB, VB>(A, job, mine, lane, q_of, o, m_ref, l);
     // ---- the four warps' sums joined ----
-    cp_wait<0>();
     __syncthreads();
     const int cpu = 16 / bv;
 #pragma unroll
@@ -582,9 +622,7 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     }
     if (!whole && u0 == 0 && tid == 0) {
       const long long end = base + (long long)(h + 1) * units;
-      A.notes[2 * blockIdx.x + 1] =
-          make_int4((int)(uint32_t)total, (int)(total >> 32), (int)(uint32_t)end, (int)(end >> 32));
-      A.notes[2 * blockIdx.x] = make_int4(b, h, 0, parts);
+      A.notes[blockIdx.x] = make_int4(b, h, 0, cs::pieces_until(total, parts, blockIdx.x, end));
     }
     w += u1 - u0;
   }

@@ -217,7 +217,7 @@ __device__ __forceinline__ void raw_load(RawRegs& r, const unsigned char* codes,
 
 // rows `row16` .. + 15 of the operand tile
 template <int BITS, int D>
-__device__ __forceinline__ void raw_store(const RawRegs& r, uint32_t tile, int row16, int lane) {
+__device__ __forceinline__ void raw_store(const RawRegs& r, uint32_t tile, int row16, int lane, uint32_t magic) {
   using W = Raw<BITS, D>;
   constexpr int PER = 32 / BITS;                // codes of a word
 #pragma unroll
@@ -231,7 +231,7 @@ __device__ __forceinline__ void raw_store(const RawRegs& r, uint32_t tile, int r
       const __half2 sc = __hmul2(ca::u2h(r.scale[i * W::BLKS + k * PER / 16]), __float2half2_rn(0.5f));
       const __half2 lo = __low2half2(sc), step = __high2half2(sc);
 #pragma unroll
-      for (int p = 0; p < PER / 2; ++p) h[k * PER / 2 + p] = ca::h2u(__hfma2(ca::code_pair<BITS>(words[k], p), step, lo));
+      for (int p = 0; p < PER / 2; ++p) h[k * PER / 2 + p] = ca::h2u(__hfma2(ca::code_pair<BITS>(words[k], p, magic), step, lo));
     }
 #pragma unroll
     for (int k = 0; k < 4 * PER / 8; ++k)
@@ -249,10 +249,11 @@ __device__ __forceinline__ void load_bits(RawRegs& r, const CacheArgs& c, int kv
   else raw_load<2, D>(r, codes, scales, lane, live);
 }
 template <int D>
-__device__ __forceinline__ void store_bits(const RawRegs& r, int bits, uint32_t tile, int row16, int lane) {
-  if (bits == 4) raw_store<4, D>(r, tile, row16, lane);
-  else if (bits == 8) raw_store<8, D>(r, tile, row16, lane);
-  else raw_store<2, D>(r, tile, row16, lane);
+__device__ __forceinline__ void store_bits(const RawRegs& r, int bits, uint32_t tile, int row16, int lane,
+                                           uint32_t magic) {
+  if (bits == 4) raw_store<4, D>(r, tile, row16, lane, magic);
+  else if (bits == 8) raw_store<8, D>(r, tile, row16, lane, magic);
+  else raw_store<2, D>(r, tile, row16, lane, magic);
 }
 }  // namespace ct
 
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    A.notes[2 * blockIdx.x] = make_int4(0, 0, -1, 0);
+    A.notes[blockIdx.x] = make_int4(0, 0, -1, 0);
   }
   // ---- this block's range of units ----
   long long total = 0;
@@ -351,6 +352,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   if (warp >= 8) {
     // ================= dequantising warps =================
     const int grp = warp - 8;                  // tokens 16 grp .. + 15 of every tile
+    const uint32_t magic = ca::magic1024();
     RawRegs rk, rv;
     int tile = jobs.u0, j = 0;                 // tile of the job; its number in this block's part
     bool more = jobs.w < jobs.w1;
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
       const int x = j & 1;
       const unsigned now_live = live;
       if (uses[x]) wait_warp(s_done(x), (uses[x] - 1) & 1);
-      store_bits<D>(rk, A.c.bits[0], sma + S::K + x * S::OPND, 16 * grp, lane);
+      store_bits<D>(rk, A.c.bits[0], sma + S::K + x * S::OPND, 16 * grp, lane, magic);
       if (lane == 0) dead[(2 * x + (uses[x] & 1)) * 8 + grp] = (uint16_t)(0xffffu << now_live);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
         load_bits<D>(rk, A.c, 0, row, lane, live);
       }
       if (uses[x]) wait_warp(o_done(x), (uses[x] - 1) & 1);
-      store_bits<D>(rv, A.c.bits[1], sma + S::V + x * S::OPND, 16 * grp, lane);
+      store_bits<D>(rv, A.c.bits[1], sma + S::V + x * S::OPND, 16 * grp, lane, magic);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive(v_full(x));
@@ -675,10 +677,8 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
         rec[D + 1] = sum;
       }
       if (!whole && jobs.u0 == 0 && tid == 0) {
-        const long long end = jobs.base + jobs.units;
-        A.notes[2 * blockIdx.x + 1] =
-            make_int4((int)(uint32_t)total, (int)(total >> 32), (int)(uint32_t)end, (int)(end >> 32));
-        A.notes[2 * blockIdx.x] = make_int4(jobs.b, jobs.h, jobs.rt, parts);
+        A.notes[blockIdx.x] = make_int4(
+            jobs.b, jobs.h, jobs.rt, cs::pieces_until(total, parts, blockIdx.x, jobs.base + jobs.units));
       }
       umma::fence_before_sync();
       bar_sync(3, 256);     // O is read before the next job's first product writes it

@@ -1,0 +1,79 @@
+// Launch of the cache attention kernels: which kernel takes how many rows, how many blocks, and
+// the join behind it.  The narrow kernel's instances for every pair of bit-widths are compiled in
+// sources of their own (cache_few_d64.cu, cache_few_d128.cu), beside one another.
+#pragma once
+
+#include "cache_attend.cuh"
+#include "host.cuh"
+
+namespace jolt {
+
+// rows of one KV head that the narrow kernel takes; more go to the other one
+inline constexpr int FEW_ROWS = 32;
+
+inline constexpr int MANY_BLOCKS = 148;   // of the tensor-core kernel: one per SM
+
+// n-tiles of the narrow kernel for at most `rows` rows of a KV head
+inline int few_tiles(long long rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+// shared memory of the narrow kernel, and its blocks: as many as the GPU holds at once (by
+// registers 4, 3 or 2 per SM, by shared memory what 228 KB hold with 1 KB reserved for each)
+inline int few_smem(const CacheArgs& c, int nt) {
+  const int bk = c.bits[0], bv = c.bits[1];
+  if (c.D == 64)
+    return nt == 1 ? ca::Smem<64, 1>::bytes(bk, bv) : nt == 2 ? ca::Smem<64, 2>::bytes(bk, bv) : ca::Smem<64, 4>::bytes(bk, bv);
+  return nt == 1 ? ca::Smem<128, 1>::bytes(bk, bv) : nt == 2 ? ca::Smem<128, 2>::bytes(bk, bv) : ca::Smem<128, 4>::bytes(bk, bv);
+}
+inline int few_blocks(const CacheArgs& c, int nt) {
+  const int by_regs = nt == 1 ? 4 : nt == 2 ? 3 : 2, by_smem = 228 * 1024 / (few_smem(c, nt) + 1024);
+  return 148 * (by_regs < by_smem ? by_regs : by_smem);
+}
+
+// launch with programmatic stream serialization: the join's blocks may be scheduled while the
+// last blocks of the kernel before it run; they wait for its end before they read
+template <typename K>
+cudaError_t launch_after(K kernel, dim3 grid, int threads, const CacheAttendArgs& A, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, A);
+}
+
+
+template <int D, int NT, int KB, int VB>
+jolt_status launch_few(const CacheAttendArgs& A, cudaStream_t st) {
+  const int smem = ca::Smem<D, NT>::bytes(KB, VB), blocks = few_blocks(A.c, NT);
+  CUDA_TRY(cudaFuncSetAttribute(cache_few_rows_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  count_launch(), cache_few_rows_kernel<D, NT, KB, VB><<<blocks, ca::WARPS * 32, smem, st>>>(A);
+  CUDA_TRY(cudaGetLastError());
+  CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT, 1, 256 / D>, dim3(blocks, A.a.max_new * A.G), 256, A, st));
+  return JOLT_OK;
+}
+
+template <int D, int NT>
+jolt_status launch_few_bits(const CacheAttendArgs& A, cudaStream_t st) {
+  switch (A.c.bits[0] * 16 + A.c.bits[1]) {
+    case 0x22: return launch_few<D, NT, 2, 2>(A, st);
+    case 0x24: return launch_few<D, NT, 2, 4>(A, st);
+    case 0x28: return launch_few<D, NT, 2, 8>(A, st);
+    case 0x42: return launch_few<D, NT, 4, 2>(A, st);
+    case 0x44: return launch_few<D, NT, 4, 4>(A, st);
+    case 0x48: return launch_few<D, NT, 4, 8>(A, st);
+    case 0x82: return launch_few<D, NT, 8, 2>(A, st);
+    case 0x84: return launch_few<D, NT, 8, 4>(A, st);
+    default: return launch_few<D, NT, 8, 8>(A, st);
+  }
+}
+
+// the narrow kernel with nt n-tiles, and its join
+template <int D>
+jolt_status launch_few_rows(const CacheAttendArgs& A, int nt, cudaStream_t st);
+
+}  // namespace jolt

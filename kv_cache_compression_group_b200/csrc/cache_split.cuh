@@ -33,7 +33,7 @@ struct CacheAttendArgs {
   long long o_row, o_head;
   bool q_vec;                // rows and heads of q are 16-byte aligned
   // scratch
-  int4* notes;               // [blocks][2]: {sequence, KV head, row tile or -1, -}, {units in all, end of the job}
+  int4* notes;               // [blocks]: {sequence, KV head, row tile or -1, blocks with a piece}
   float* pieces;             // [blocks][2][rows of a tile][D + 4]: D outputs, maximum, sum
 };
 
@@ -53,6 +53,13 @@ __device__ __forceinline__ float ex2(float x) {
 
 // start of block c's range when `total` units are dealt to `parts` blocks
 __device__ __forceinline__ long long range_start(long long total, int parts, int c) { return total * c / parts; }
+// number of blocks from c0 on whose ranges begin before unit `end`
+__device__ __forceinline__ int pieces_until(long long total, int parts, int c0, long long end) {
+  int c = (int)(end * parts / total);                  // range_start(c) <= end
+  while (c > c0 && range_start(total, parts, c) >= end) --c;
+  while (c + 1 < parts && range_start(total, parts, c + 1) < end) ++c;
+  return c - c0 + 1;
+}
 }  // namespace cs
 
 // position of key t of a sequence whose new rows start at position `old` and row `row0`
@@ -100,55 +107,53 @@ __device__ __forceinline__ void store_out(const CacheAttendArgs& A, int D, int r
   else reinterpret_cast<bf16*>(A.out)[at] = __float2bfloat16_rn(y);
 }
 
-// Join the pieces of the job that begins in block blockIdx.x, 8 / SPLIT rows of its tile per CTA:
-// SPLIT of the eight warps take a row's pieces in turn, and their sums are added in warp order.
-// (A few rows of few jobs have up to 74 pieces each; 128 rows of many jobs mostly two.)
-template <int D, int ROWS, int SPLIT>
+// Join the pieces of the job that begins in block blockIdx.x, one CTA per PER rows of its tile: the
+// pieces' maxima and sums first, then the weighted sums in the pieces' order, GROUPS threads per feature
+// taking every GROUPS-th piece (a few rows of few jobs have up to 74 pieces each; 128 rows of many
+// jobs mostly two).
+template <int D, int ROWS, int PER, int GROUPS>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendArgs A) {
-  __shared__ float so[8][D], sm[8], sl[8];
+  constexpr int REC = D + 4, MOST = 592, AT_ONCE = 256 / (D * GROUPS);
+  __shared__ float2 ml[AT_ONCE][MOST];      // maximum and sum of every piece
+  __shared__ float part[AT_ONCE][GROUPS][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 note = A.notes[2 * c0];
-  const int b = note.x, h = note.y, tile = note.z, parts = note.w;
+  const int c0 = blockIdx.x, tid = threadIdx.x;
+  const int4 note = A.notes[c0];
+  const int b = note.x, h = note.y, tile = note.z, count = note.w;
   if (tile < 0) return;
-  const int mine = blockIdx.y * (8 / SPLIT) + warp / SPLIT;   // row of the tile
-  const int row = tile * ROWS + mine;
   const int row0 = A.a.starts[b], R = (A.a.starts[b + 1] - row0) * A.G;
-  const int4 note2 = A.notes[2 * c0 + 1];
-  const long long total = (long long)(uint32_t)note2.x | ((long long)note2.y << 32);
-  const long long end = (long long)(uint32_t)note2.z | ((long long)note2.w << 32);
-  constexpr int REC = D + 4, V = D / 32;
-  float o[V], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = 0.f;
-  for (int c = c0 + warp % SPLIT; row < R && c < parts && (c == c0 || cs::range_start(total, parts, c) < end);
-       c += SPLIT) {
-    const float* p = A.pieces + ((2ll * c + (c == c0 ? 1 : 0)) * ROWS + mine) * REC;
-    const float pm = p[D], pl = p[D + 1], top = fmaxf(m, pm);
-    const float f = l == 0.f ? 0.f : cs::ex2(m - top), g = pl == 0.f ? 0.f : cs::ex2(pm - top);
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = fmaf(g, p[lane * V + i], f * o[i]);
-    l = fmaf(g, pl, f * l);
-    m = top;
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) so[warp][lane * V + i] = o[i];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < 8 / SPLIT * D; idx += 256) {
-    const int first = idx / D * SPLIT, d = idx % D, out = tile * ROWS + blockIdx.y * (8 / SPLIT) + idx / D;
-    if (out >= R) break;
-    float top = -INFINITY, y = 0.f, sum = 0.f;
-    for (int w = first; w < first + SPLIT; ++w) top = fmaxf(top, sm[w]);
-    for (int w = first; w < first + SPLIT; ++w) {
-      const float f = sl[w] == 0.f ? 0.f : cs::ex2(sm[w] - top);
-      y = fmaf(f, so[w][d], y);
-      sum = fmaf(f, sl[w], sum);
+  const int slot = tid / (D * GROUPS), grp = tid / D % GROUPS, d = tid % D, t = tid % (D * GROUPS);
+  // record of row `mine` in the k-th piece
+  auto rec = [&](int mine, int k) { return A.pieces + ((2ll * (c0 + k) + (k == 0 ? 1 : 0)) * ROWS + mine) * REC; };
+  for (int first = 0; first < PER; first += AT_ONCE) {
+    const int mine = blockIdx.y * PER + first + slot, row = tile * ROWS + mine;
+    float top = -INFINITY, sum = 0.f, y = 0.f;
+    if (row < R)
+      for (int k = t; k < count; k += D * GROUPS) ml[slot][k] = *reinterpret_cast<const float2*>(rec(mine, k) + D);
+    __syncthreads();
+    if (row < R) {
+#pragma unroll 8
+      for (int k = 0; k < count; ++k) top = fmaxf(top, ml[slot][k].x);
+#pragma unroll 8
+      for (int k = 0; k < count; ++k) {
+        const float2 x = ml[slot][k];
+        const float f = x.y == 0.f ? 0.f : cs::ex2(x.x - top);
+        sum = fmaf(f, x.y, sum);
+      }
+#pragma unroll 8
+      for (int k = grp; k < count; k += GROUPS) {
+        const float2 x = ml[slot][k];
+        y = fmaf(x.y == 0.f ? 0.f : cs::ex2(x.x - top), rec(mine, k)[d], y);
+      }
+      part[slot][grp][d] = y;
     }
-    store_out(A, D, row0 + out / A.G, h * A.G + out % A.G, d, y, sum, top);
+    __syncthreads();
+    if (row < R && grp == 0) {
+#pragma unroll
+      for (int k = 1; k < GROUPS; ++k) y += part[slot][k][d];
+      store_out(A, D, row0 + row / A.G, h * A.G + row % A.G, d, y, sum, top);
+    }
+    __syncthreads();
   }
 }
 

@@ -59,7 +59,7 @@ jolt_status cache_args(const jolt_cache* c, const jolt_cache_batch* b, CacheArgs
 template <typename T>
 RowsArgs<T> rows_args(T* k, T* v, int64_t kr, int64_t kh, int64_t vr, int64_t vh) {
   const int64_t per = 16 / sizeof(T);
-  RowsArgs<T> x;
+  RowsArgs<T> x{};
   x.x[0] = k;
   x.x[1] = v;
   x.row[0] = kr;
@@ -71,18 +71,31 @@ RowsArgs<T> rows_args(T* k, T* v, int64_t kr, int64_t kh, int64_t vr, int64_t vh
   return x;
 }
 
+// rows of a warp: enough that what is found once per warp is spread over several, few enough that
+// every SM has its warps
 template <typename T>
-jolt_status launch_write(const CacheArgs& c, const BatchArgs& a, const RowsArgs<const T>& x, cudaStream_t st) {
-  const long long blocks = (long long)a.rows * c.H * (c.D / pc::BLK);
-  count_launch(), cache_write_kernel<T><<<dim3((unsigned)ceil_div(blocks, 256), 2), 256, 0, st>>>(c, a, x);
+dim3 rows_grid(const CacheArgs& c, const BatchArgs& a, RowsArgs<T>* x) {
+  const long long groups = ceil_div(c.H, 512 / c.D), fit = (long long)a.rows * groups * 2 / (148 * 48);
+  x->per_warp = (int)(fit < 1 ? 1 : fit > 8 ? 8 : fit);
+  return dim3((unsigned)ceil_div(a.rows, ROW_WARPS * x->per_warp), (unsigned)groups, 2);
+}
+
+template <typename T>
+jolt_status launch_write(const CacheArgs& c, const BatchArgs& a, RowsArgs<const T> x, cudaStream_t st) {
+  const dim3 grid = rows_grid(c, a, &x);
+  count_launch();
+  if (c.D == 64) cache_write_kernel<T, 64><<<grid, ROW_WARPS * 32, 0, st>>>(c, a, x);
+  else cache_write_kernel<T, 128><<<grid, ROW_WARPS * 32, 0, st>>>(c, a, x);
   CUDA_TRY(cudaGetLastError());
   return JOLT_OK;
 }
 
 template <typename T>
-jolt_status launch_read(const CacheArgs& c, const BatchArgs& a, const RowsArgs<T>& x, cudaStream_t st) {
-  const long long blocks = (long long)a.rows * c.H * (c.D / pc::BLK);
-  count_launch(), cache_read_kernel<T><<<dim3((unsigned)ceil_div(blocks, 256), 2), 256, 0, st>>>(c, a, x);
+jolt_status launch_read(const CacheArgs& c, const BatchArgs& a, RowsArgs<T> x, cudaStream_t st) {
+  const dim3 grid = rows_grid(c, a, &x);
+  count_launch();
+  if (c.D == 64) cache_read_kernel<T, 64><<<grid, ROW_WARPS * 32, 0, st>>>(c, a, x);
+  else cache_read_kernel<T, 128><<<grid, ROW_WARPS * 32, 0, st>>>(c, a, x);
   CUDA_TRY(cudaGetLastError());
   return JOLT_OK;
 }

@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
           if (!is) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = 0.f;
-          } else if (A.q_f16) load16(reinterpret_cast<const __half*>(A.q) + at + 16 * k, vec, v);
-          else load16(reinterpret_cast<const bf16*>(A.q) + at + 16 * k, vec, v);
+          } else if (A.q_f16) load_n(reinterpret_cast<const __half*>(A.q) + at + 16 * k, vec, v);
+          else load_n(reinterpret_cast<const bf16*>(A.q) + at + 16 * k, vec, v);
 #pragma unroll
           for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[e]));
         }
@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
           if (!is) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = 0.f;
-          } else if (A.q_f16) load16(reinterpret_cast<const __half*>(A.q) + at + 16 * k, vec, v);
-          else load16(reinterpret_cast<const bf16*>(A.q) + at + 16 * k, vec, v);
+          } else if (A.q_f16) load_n(reinterpret_cast<const __half*>(A.q) + at + 16 * k, vec, v);
+          else load_n(reinterpret_cast<const bf16*>(A.q) + at + 16 * k, vec, v);
           uint32_t h[8];
           const int bk = A.c.bits[0];
 #pragma unroll

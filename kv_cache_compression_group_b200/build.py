@@ -10,15 +10,13 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libjolt.so")
-SOURCES = ["jolt_api.cu", "cache_api.cu", "cache_few_d64.cu", "cache_few_d128.cu"]
+SOURCES = ["jolt_api.cu", "cache_api.cu", "cache_few_d64.cu", "cache_few_d128.cu",
+           "cache_many_d64.cu", "cache_many_d128.cu"]
 DEPS = ["jolt_api.cu", "common.cuh", "gemm.cuh", "kernels.cuh", "misc.cuh", "umma.cuh", "eig_cluster.cuh", "chol.cuh",
         "fp16_exact.cuh", "table_tc.cuh", "attend.cuh", "eig_large.cuh", "host.cuh", "cache_api.cu", "cache.cuh", "cache_split.cuh",
-        "cache_attend.cuh", "cache_attend_tc.cuh", "cache_launch.cuh", "cache_few_d64.cu", "cache_few_d128.cu"]
-# a source is rebuilt when any file changes that is not listed here as none of its own
-CACHE = [d for d in DEPS if d.startswith("cache")]
-NOT_OF = {"jolt_api.cu": CACHE, "cache_api.cu": ["jolt_api.cu", "cache_few_d64.cu", "cache_few_d128.cu"],
-          "cache_few_d64.cu": ["jolt_api.cu", "cache_api.cu", "cache_few_d128.cu", "cache_attend_tc.cuh"],
-          "cache_few_d128.cu": ["jolt_api.cu", "cache_api.cu", "cache_few_d64.cu", "cache_attend_tc.cuh"]}
+        "cache_attend.cuh", "cache_attend_tc.cuh", "cache_launch.cuh",
+        "cache_few_d64.cu", "cache_few_d128.cu", "cache_many_d64.cu", "cache_many_d128.cu"]
+CACHE = [d for d in DEPS if d.startswith("cache") and d.endswith(".cuh")]
 
 
 def nvcc_cmd(source: str, out: str, extra=()) -> list:
@@ -39,9 +37,9 @@ def _newer(target: str, paths) -> bool:
 
 
 def _inputs(source: str) -> list:
-    """Files whose change rebuilds a source's object."""
-    deps = [d for d in DEPS if d not in NOT_OF[source]]
-    return [os.path.join(CSRC, d) for d in deps] + [os.path.join(ROOT, "include", "jolt.h")]
+    """Files whose change rebuilds a source's object: all headers, but the cache's own for the cache alone."""
+    headers = [d for d in DEPS if d.endswith(".cuh") and (d not in CACHE or source.startswith("cache"))]
+    return [os.path.join(CSRC, d) for d in [source] + headers] + [os.path.join(ROOT, "include", "jolt.h")]
 
 
 def up_to_date() -> bool:

@@ -6,7 +6,6 @@
 #include "host.cuh"
 #include "cache.cuh"
 #include "cache_launch.cuh"
-#include "cache_attend_tc.cuh"
 
 using namespace jolt;
 
@@ -106,7 +105,7 @@ struct Scratch {
 Scratch attend_scratch(const CacheArgs& c, const BatchArgs& a, int nq) {
   const long long rows = (long long)a.max_new * (nq / c.H);
   const int nt = few_tiles(rows);
-  const size_t blocks = rows > FEW_ROWS ? MANY_BLOCKS : few_blocks(c, nt), tile = rows > FEW_ROWS ? ct::ROWS : 8 * nt;
+  const size_t blocks = rows > FEW_ROWS ? MANY_BLOCKS : few_blocks(c, nt), tile = rows > 128 ? 256 : rows > FEW_ROWS ? 128 : 8 * nt;
   Scratch s;
   Bump m;
   s.notes = m.take(sizeof(int4) * blocks);
@@ -119,12 +118,7 @@ template <int D>
 jolt_status launch_cache_attend(const CacheAttendArgs& A, cudaStream_t st) {
   const long long rows = (long long)A.a.max_new * A.G;
   if (rows <= FEW_ROWS) return launch_few_rows<D>(A, few_tiles(rows), st);
-  constexpr int smem = ct::Smem<D>::BYTES;
-  CUDA_TRY(cudaFuncSetAttribute(cache_many_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  count_launch(), cache_many_rows_kernel<D><<<MANY_BLOCKS, ct::THREADS, smem, st>>>(A);
-  CUDA_TRY(cudaGetLastError());
-  CUDA_TRY(launch_after(cache_join_kernel<D, ct::ROWS, 8, 1>, dim3(MANY_BLOCKS, ct::ROWS / 8), 256, A, st));
-  return JOLT_OK;
+  return launch_many_rows<D>(A, rows > 128, st);
 }
 
 }  // namespace
@@ -224,6 +218,7 @@ jolt_status jolt_cache_attend(const jolt_cache* cache, const jolt_cache_batch* b
   A.q_f16 = dtype == JOLT_F16;
   A.q_row = q_row_stride;
   A.q_head = q_head_stride;
+  A.o_vec = aligned16(out_dev) && out_row_stride % 8 == 0 && out_head_stride % 8 == 0;
   A.q_vec = aligned16(q_dev) && q_row_stride % 8 == 0 && q_head_stride % 8 == 0;
   A.out = out_dev;
   A.o_row = out_row_stride;

@@ -429,6 +429,8 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
   unsigned char* mine = ring + warp * stages(D, bk, bv) * stage_bytes(D, bk, bv);
   int row0, n, len, first;
 
+  cs::wait_for_predecessor();
+  cs::let_successor_start();
   // ---- this block's range of units: all units, then the sequence in which the range begins ----
   long long total = 0;
   for (int b = tid; b < A.a.B; b += WARPS * 32)

@@ -1,22 +1,24 @@
 // Attention of many rows per KV head (wide trees, chunks of a prompt) over the paged cache, on the
 // 5th-generation tensor cores.
 //
-// A job is 128 rows (new row x query head) of one KV head; its keys come in tiles of 128 tokens.
-// One persistent CTA of 16 warps per SM:
+// A job is 128 rows (new row x query head) of one KV head, or 256 where there are more; its keys come
+// in tiles of 128 tokens.  One persistent CTA of 16 warps per SM:
 //   * eight dequantising warps take 16 tokens of every tile each: packed codes and (lo, step) pairs
-//     straight to registers, one tile ahead, then fp16(lo / 2 + code * (step / 2)) into the
-//     128-byte-swizzled operand tiles.  The features of a row keep the order in which a packed
-//     word gives its pairs; Q is laid out in the same order, the output columns are put back.
-//   * two softmax warpgroups take the even and the odd tiles of the job, each with operand tiles,
-//     score and output accumulators, maximum and sum of its own (all 512 columns of tensor
-//     memory), so that one group's exponentials overlap the other's products.  A thread has one
-//     row: it reads its scores twice (maximum, then weights), writes the weights as fp16 over the
-//     scores, and when its group has, one elected thread issues O += P V (P from tensor memory)
-//     and the group's next S = Q K^T.  The reference maximum may lag by 2^8, so rescaling O, a pass
-//     through tensor memory, is rare after the first tiles.
-//   * at the end both groups' outputs are joined, half of the columns by each group.
-// What bounds it at D = 128: the two products take 1024 cycles per tile, its 16384 exponentials
-// 1024 at 16 per cycle, and the instructions of softmax and dequantisation about 1200 per scheduler.
+//     straight to registers, one tile ahead (and the page's number two), then
+//     fp16(lo / 2 + code * (step / 2)) into the 128-byte-swizzled operand tiles, two of K and two of V.
+//     The features of a row keep the order in which a packed word gives its pairs; Q is laid out in
+//     the same order, the output columns are put back.
+//   * two softmax warpgroups with score and output accumulators of their own (all 512 columns of
+//     tensor memory), so that one group's exponentials overlap the other's products.  With 256 rows
+//     each has 128 of them and both use every tile, which halves the dequantisation; with 128 rows
+//     one takes the even and the other the odd tiles, joined at the end.  A thread has one row: it
+//     reads its scores twice (maximum, then weights), writes the weights as fp16 over the scores, and
+//     when its group has, one elected thread issues O += P V (P from tensor memory) and the group's
+//     next S = Q K^T.  The reference maximum may lag by 2^8, so rescaling O, a pass through tensor
+//     memory, is rare after the first tiles.
+// What bounds it at D = 128: the two products take 1024 cycles per 128 x 128 tile, its 16384
+// exponentials 1024 at 16 per cycle, and the instructions of softmax (about 450 per scheduler) and
+// of dequantisation (about 600, once per 256 rows) come next to them.
 //
 // Every wait is bounded; after one gave up, the roles keep their barrier schedule without waiting or
 // issuing, so the CTA ends, and the issued products are drained before tensor memory is freed.
@@ -27,14 +29,14 @@
 
 namespace jolt {
 namespace ct {
-constexpr int ROWS = 128, TILE = 128;
+constexpr int TILE = 128;
 constexpr int THREADS = 512;
 constexpr int BOX = 128 * 128;                 // bytes of 128 rows x 64 fp16 features
 template <int D>
 struct Smem {
   static constexpr int OPND = D / 64 * BOX;    // bytes of a 128 x D operand tile
-  static constexpr int Q = 0, K = OPND, V = 3 * OPND, MISC = 5 * OPND;
-  static constexpr int BYTES = MISC + 4096 + 1024;
+  static constexpr int Q = 0, K = OPND, V = 3 * OPND, Q2 = 5 * OPND;
+  static constexpr int bytes(bool pair) { return (pair ? 6 : 5) * OPND + 1024; }
 };
 // fp16 A and B, fp32 accumulator, M = 128
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
@@ -63,14 +65,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
         "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
-      ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   __syncwarp();
@@ -82,19 +76,81 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// umma::mbar_wait with a hint that lets the thread sleep for longer between its looks
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = umma::global_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (umma::global_ns() - t0 > umma::kWaitNs) return false;
+  }
+}
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// the values of earlier loads may be used after this; they pass through it so that no use moves up
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&a)[32], uint32_t (&b)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]),
+                 "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]),
+                 "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15])
+               :
+               : "memory");
+  asm volatile(""
+               : "+r"(b[16]), "+r"(b[17]), "+r"(b[18]), "+r"(b[19]), "+r"(b[20]), "+r"(b[21]), "+r"(b[22]), "+r"(b[23]),
+                 "+r"(b[24]), "+r"(b[25]), "+r"(b[26]), "+r"(b[27]), "+r"(b[28]), "+r"(b[29]), "+r"(b[30]), "+r"(b[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+      ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
+        "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
+        "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+      : "memory");
+}
 // 16-byte piece `piece` (8 features) of row `row` of an operand tile
 __device__ __forceinline__ uint32_t piece_addr(uint32_t tile, int row, int piece) {
   return tile + (piece >> 3) * BOX + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 // feature at place p of a row as the dequantised words hold it
-__device__ __forceinline__ int feature_at(int bits, int p) {
+__device__ __forceinline__ constexpr int feature_at(int bits, int p) {
   const int per = 32 / bits, in = p & (per - 1);
   return (p - in) + (in >> 1) + (in & 1) * (per >> 1);
 }
 
-// one sequence's jobs
+// one sequence's jobs, of ROWS rows
+template <int ROWS>
 struct Seq {
-  int row0, n, len, first, tiles;      // tiles: of 128 rows
+  int row0, n, len, first, tiles;      // tiles: of ROWS rows
   bool causal;
   // units of row tile rt: the keys that any of its rows may see
   __device__ int units(const CacheAttendArgs& A, int rt) const {
@@ -103,15 +159,17 @@ struct Seq {
     return (end - first + TILE - 1) / TILE;
   }
 };
-__device__ __forceinline__ bool load_seq(const CacheAttendArgs& A, int b, Seq& s) {
+template <int ROWS>
+__device__ __forceinline__ bool load_seq(const CacheAttendArgs& A, int b, Seq<ROWS>& s) {
   const int u = cache_units(A, b, TILE, s.row0, s.n, s.len, s.first);
   if (u == 0) return false;
   s.tiles = (int)(((long long)s.n * A.G + ROWS - 1) / ROWS);
   s.causal = A.mask == nullptr;
   return true;
 }
+template <int ROWS>
 __device__ __forceinline__ long long seq_units(const CacheAttendArgs& A, int b) {
-  Seq s;
+  Seq<ROWS> s;
   if (!load_seq(A, b, s)) return 0;
   if (!s.causal) return (long long)s.tiles * s.units(A, 0);
   long long sum = 0;
@@ -120,10 +178,11 @@ __device__ __forceinline__ long long seq_units(const CacheAttendArgs& A, int b) 
 }
 
 // The jobs of a block's range [w, w1), in order; every thread walks its own copy.
+template <int ROWS>
 struct Jobs {
   long long w, w1, base;   // base: first unit of (b, h, rt)
   int b, h, rt;
-  Seq s;
+  Seq<ROWS> s;
   int units, u0, u1;       // of the job, and of this block's part of it
   __device__ void start(const CacheAttendArgs& A, long long from, long long to, int b0, long long b0_base) {
     w = from;
@@ -133,7 +192,7 @@ struct Jobs {
     h = rt = 0;
     if (w >= w1) return;
     load_seq(A, b, s);
-    const long long per = seq_units(A, b);
+    const long long per = seq_units<ROWS>(A, b);
     h = (int)((w - base) / per);
     base += h * per;
     settle(A);
@@ -188,31 +247,45 @@ struct RawRegs {
   uint32_t scale[4];
 };
 
-template <int BITS, int D>
-__device__ __forceinline__ void raw_load(RawRegs& r, const unsigned char* codes, const __half2* scales, int lane,
-                                         int live) {
+template <int BITS, int D, bool ALL>
+__device__ __forceinline__ void raw_load_rows(RawRegs& r, const unsigned char* codes, const __half2* scales, int lane,
+                                              int live) {
   using W = Raw<BITS, D>;
 #pragma unroll
   for (int i = 0; i < W::N; ++i) {
     const int row = W::row(lane, i), ch = W::chunk(lane, i);
-    r.code[i] = make_uint4(0u, 0u, 0u, 0u);
-    const bool on = row < live && (W::CH > 1 || lane < 16);
-    if (on) r.code[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * (D * BITS / 8) + ch * 16));
+    const bool on = (ALL || row < live) && (W::CH > 1 || lane < 16);
+    const uint4* src = reinterpret_cast<const uint4*>(codes + row * (D * BITS / 8) + ch * 16);
     const uint32_t* sc = reinterpret_cast<const uint32_t*>(scales + row * (D / 16) + ch * W::BLKS);
+    if (!on) {
+      r.code[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < W::BLKS; ++k) r.scale[i * W::BLKS + k] = 0u;
+      continue;
+    }
+    r.code[i] = __ldg(src);
     if constexpr (W::BLKS == 1) {
-      r.scale[i] = on ? __ldg(sc) : 0u;
+      r.scale[i] = __ldg(sc);
     } else if constexpr (W::BLKS == 2) {
-      const uint2 v = on ? __ldg(reinterpret_cast<const uint2*>(sc)) : make_uint2(0u, 0u);
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(sc));
       r.scale[2 * i] = v.x;
       r.scale[2 * i + 1] = v.y;
     } else {
-      const uint4 v = on ? __ldg(reinterpret_cast<const uint4*>(sc)) : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(sc));
       r.scale[0] = v.x;
       r.scale[1] = v.y;
       r.scale[2] = v.z;
       r.scale[3] = v.w;
     }
   }
+}
+template <int BITS, int D>
+__device__ __forceinline__ void raw_load(RawRegs& r, const unsigned char* codes, const __half2* scales, long long row,
+                                         int lane, int live) {
+  codes += row * (D * BITS / 8);
+  scales += row * (D / 16);
+  if (live == 16) raw_load_rows<BITS, D, true>(r, codes, scales, lane, live);
+  else raw_load_rows<BITS, D, false>(r, codes, scales, lane, live);
 }
 
 // rows `row16` .. + 15 of the operand tile
@@ -239,50 +312,84 @@ __device__ __forceinline__ void raw_store(const RawRegs& r, uint32_t tile, int r
   }
 }
 
-template <int D>
-__device__ __forceinline__ void load_bits(RawRegs& r, const CacheArgs& c, int kv, long long row, int lane, int live) {
-  const int bits = c.bits[kv];
-  const unsigned char* codes = c.codes[kv] + row * (D * bits / 8);
-  const __half2* scales = c.scales[kv] + row * (D / 16);
-  if (bits == 4) raw_load<4, D>(r, codes, scales, lane, live);
-  else if (bits == 8) raw_load<8, D>(r, codes, scales, lane, live);
-  else raw_load<2, D>(r, codes, scales, lane, live);
-}
-template <int D>
-__device__ __forceinline__ void store_bits(const RawRegs& r, int bits, uint32_t tile, int row16, int lane,
-                                           uint32_t magic) {
-  if (bits == 4) raw_store<4, D>(r, tile, row16, lane, magic);
-  else if (bits == 8) raw_store<8, D>(r, tile, row16, lane, magic);
-  else raw_store<2, D>(r, tile, row16, lane, magic);
-}
 }  // namespace ct
 
-template <int D>
+// 32 outputs of a row from place c0 on, in the order of the dequantised words: put back in order and
+// stored (see store_out), or left as a piece
+template <int D, int VB>
+__device__ __forceinline__ void store_places(const CacheAttendArgs& A, int r, int j, int c0, const float (&v)[32],
+                                             float l, float m) {
+  float y[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) y[ct::feature_at(VB, e)] = v[e];
+  if (A.prefix_out) {
+    const float lp = A.prefix_lse[(long long)r * A.nq + j] * cs::LOG2E, top = fmaxf(m, lp);
+    const float f = l == 0.f ? 0.f : cs::ex2(m - top);
+    const float g = lp == -INFINITY ? 0.f : cs::ex2(lp - top + cs::SHIFT);
+    const float* o = A.prefix_out + ((long long)r * A.nq + j) * D + c0;
+    l = fmaf(f, l, g);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) y[e] = g != 0.f ? fmaf(g, o[e], f * y[e]) : f * y[e];
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const long long at = r * A.o_row + j * A.o_head + c0;
+  uint32_t h[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float a = l != 0.f ? y[2 * e] * inv : 0.f, b = l != 0.f ? y[2 * e + 1] * inv : 0.f;
+    if (A.q_f16) {
+      h[e] = ca::h2u(__floats2half2_rn(a, b));
+    } else {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+      h[e] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+  }
+  uint16_t* out = reinterpret_cast<uint16_t*>(A.out) + at;
+  if (A.o_vec) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      reinterpret_cast<uint4*>(out)[e] = make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      out[2 * e] = (uint16_t)h[e];
+      out[2 * e + 1] = (uint16_t)(h[e] >> 16);
+    }
+  }
+}
+
+// PAIR: jobs of 256 rows, 128 for each softmax group, which both use every tile; else jobs of 128
+// rows, whose even tiles are the one group's and whose odd tiles the other's.  Tile j of a job lies in
+// operand buffers j % 2 either way.
+template <int D, int KB, int VB, bool PAIR>
 __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAttendArgs A) {
   using namespace ct;
   using S = Smem<D>;
+  constexpr int ROWS = PAIR ? 256 : 128;
   extern __shared__ unsigned char ct_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)ct_raw + 1023) & ~(uintptr_t)1023);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::MISC);      // 10 barriers
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::MISC + 96);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 100);
-  volatile uint16_t* dead = reinterpret_cast<volatile uint16_t*>(sm + S::MISC + 128);   // [group][parity][8]
-  long long* s_sum = reinterpret_cast<long long*>(sm + S::MISC + 256);                  // [16]
-  long long* s_base = s_sum + 16;
-  int* s_b = reinterpret_cast<int*>(s_base + 1);
-  float* s_max = reinterpret_cast<float*>(sm + S::MISC + 512);                          // [2][128]
-  float* s_ml = s_max + 256;                                                            // [2][128][2]
+  __shared__ __align__(8) uint64_t bars[14];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int aborted, s_b;
+  __shared__ long long s_sum[16], s_base;
+  __shared__ __align__(16) uint16_t s_dead[2][2][8];      // [buffer][parity of its use][16 tokens each]
+  __shared__ float s_max[2][2][128];                      // largest |q| of [group][half of the features][row]
+  __shared__ float2 s_ml[2][128];                         // maximum and sum of [group][row]
+  volatile int* abort_flag = &aborted;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sma = umma::smem_u32(sm), bar0 = umma::smem_u32(bars);
-  // barriers of group x: K tile written, S = Q K^T done, V tile written, O += P V done
-  auto k_full = [&](int x) { return bar0 + 8 * x; };
-  auto s_done = [&](int x) { return bar0 + 16 + 8 * x; };
-  auto v_full = [&](int x) { return bar0 + 32 + 8 * x; };
-  auto o_done = [&](int x) { return bar0 + 48 + 8 * x; };
-  auto drain = [&](int x) { return bar0 + 64 + 8 * x; };
+  // barriers of buffer i: K written, K no longer needed, V written, V no longer needed; of group x:
+  // S = Q K^T done, O += P V done, all done
+  auto k_full = [&](int i) { return bar0 + 8 * i; };
+  auto k_free = [&](int i) { return bar0 + 16 + 8 * i; };
+  auto v_full = [&](int i) { return bar0 + 32 + 8 * i; };
+  auto v_free = [&](int i) { return bar0 + 48 + 8 * i; };
+  auto s_done = [&](int x) { return bar0 + 64 + 8 * x; };
+  auto o_done = [&](int x) { return bar0 + 80 + 8 * x; };
+  auto drain = [&](int x) { return bar0 + 96 + 8 * x; };
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (*abort_flag) return false;
-    if (umma::mbar_wait(bar, parity)) return true;
+    if (ct::mbar_wait(bar, parity)) return true;
     *abort_flag = 1;
     return false;
   };
@@ -292,21 +399,25 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   };
 
   if (tid == 0) {
-    for (int x = 0; x < 2; ++x) {
-      umma::mbar_init(k_full(x), 8);
-      umma::mbar_init(s_done(x), 1);
-      umma::mbar_init(v_full(x), 8);
-      umma::mbar_init(o_done(x), 1);
-      umma::mbar_init(drain(x), 1);
+    for (int i = 0; i < 2; ++i) {
+      umma::mbar_init(k_full(i), 8);
+      umma::mbar_init(k_free(i), PAIR ? 2 : 1);
+      umma::mbar_init(v_full(i), 8);
+      umma::mbar_init(v_free(i), PAIR ? 2 : 1);
+      umma::mbar_init(s_done(i), 1);
+      umma::mbar_init(o_done(i), 1);
+      umma::mbar_init(drain(i), 1);
     }
-    *abort_flag = 0;
+    aborted = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    A.notes[blockIdx.x] = make_int4(0, 0, -1, 0);
   }
+  cs::wait_for_predecessor();
+  cs::let_successor_start();
+  if (tid == 0) A.notes[blockIdx.x] = make_int4(0, 0, -1, 0);
   // ---- this block's range of units ----
   long long total = 0;
-  for (int b = tid; b < A.a.B; b += THREADS) total += seq_units(A, b) * A.c.H;
+  for (int b = tid; b < A.a.B; b += THREADS) total += seq_units<ROWS>(A, b) * A.c.H;
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
   if (lane == 0) s_sum[warp] = total;
@@ -320,7 +431,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
     long long base = 0;
     for (int b0 = 0; b0 < A.a.B; b0 += 32) {
       const int b = b0 + lane;
-      const long long u = b < A.a.B ? seq_units(A, b) * A.c.H : 0;
+      const long long u = b < A.a.B ? seq_units<ROWS>(A, b) * A.c.H : 0;
       long long sum = u;
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
@@ -330,14 +441,14 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
       const unsigned hit = __ballot_sync(0xffffffffu, base + sum > w0);
       if (hit) {
         if (lane == __ffs(hit) - 1) {
-          *s_b = b;
-          *s_base = base + sum - u;
+          s_b = b;
+          s_base = base + sum - u;
         }
         break;
       }
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(umma::smem_u32(tmem_slot)),
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(umma::smem_u32(&tmem_slot)),
                  "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -345,177 +456,200 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
-  Jobs jobs;
-  jobs.start(A, w0, w1, *s_b, *s_base);
+  const uint32_t tmem = tmem_slot;
+  Jobs<ROWS> jobs;
+  jobs.start(A, w0, w1, s_b, s_base);
 
   if (warp >= 8) {
     // ================= dequantising warps =================
     const int grp = warp - 8;                  // tokens 16 grp .. + 15 of every tile
     const uint32_t magic = ca::magic1024();
+    const unsigned char* const kc = A.c.codes[0];
+    const unsigned char* const vc = A.c.codes[1];
+    const __half2* const ks = A.c.scales[0];
+    const __half2* const vs = A.c.scales[1];
     RawRegs rk, rv;
-    int tile = jobs.u0, j = 0;                 // tile of the job; its number in this block's part
-    bool more = jobs.w < jobs.w1;
     uint32_t uses[2] = {0u, 0u};
-    unsigned live = 0;                         // tokens of the 16 that exist
-    long long row = 0;
-    auto locate = [&]() {                      // the current tile's rows in the pool
+    // The walk over the tiles runs ahead: `ahead` is the tile whose page number is being looked up.
+    int tile = jobs.u0, j = 0;                 // of the job; its number in this block's part
+    int num = 0;                               // page number of that tile's 16 tokens
+    auto look_up = [&]() {
+      const int t = jobs.s.first + tile * TILE + 16 * grp;
+      num = t < jobs.s.len ? A.a.table[(long long)jobs.b * A.a.max_pages + (t >> A.c.page_shift)] : -1;
+    };
+    auto resolve = [&](long long& row, int& live, int& buf) {   // where that tile's rows are; then on to the next
       const int t = jobs.s.first + tile * TILE + 16 * grp;
       live = 0;
+      buf = j & 1;
       if (t < jobs.s.len) {
-        const int page = page_at(A.a, A.c, jobs.b, t);
-        if (page >= 0) {
-          row = row_index(A.c, page, jobs.h, t);
+        if ((unsigned)num < (unsigned)A.c.n_pages) {
+          row = row_index(A.c, num, jobs.h, t);
           live = min(16, jobs.s.len - t);
+        } else {
+          raise_status(A.a.status, DEV_ERR_BATCH);
         }
       }
-    };
-    if (more) {
-      locate();
-      load_bits<D>(rk, A.c, 0, row, lane, live);
-      load_bits<D>(rv, A.c, 1, row, lane, live);
-    }
-    while (more) {
-      const int x = j & 1;
-      const unsigned now_live = live;
-      if (uses[x]) wait_warp(s_done(x), (uses[x] - 1) & 1);
-      store_bits<D>(rk, A.c.bits[0], sma + S::K + x * S::OPND, 16 * grp, lane, magic);
-      if (lane == 0) dead[(2 * x + (uses[x] & 1)) * 8 + grp] = (uint16_t)(0xffffu << now_live);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) arrive(k_full(x));
-      // the next tile, its keys under way before the values of this one
       ++tile;
       ++j;
       if (tile == jobs.u1) {
         jobs.next(A);
-        more = jobs.w < jobs.w1;
         tile = jobs.u0;
         j = 0;
       }
-      if (more) {
-        locate();
-        load_bits<D>(rk, A.c, 0, row, lane, live);
-      }
-      if (uses[x]) wait_warp(o_done(x), (uses[x] - 1) & 1);
-      store_bits<D>(rv, A.c.bits[1], sma + S::V + x * S::OPND, 16 * grp, lane, magic);
+      if (jobs.w < jobs.w1) look_up();
+    };
+    long long row = 0, row1 = 0;
+    int live, live1 = 0, buf, buf1 = 0;
+    look_up();
+    resolve(row, live, buf);
+    raw_load<KB, D>(rk, kc, ks, row, lane, live);
+    raw_load<VB, D>(rv, vc, vs, row, lane, live);
+    bool have1 = jobs.w < jobs.w1;             // a tile after the one in hand
+    if (have1) resolve(row1, live1, buf1);
+    for (;;) {
+      if (uses[buf]) wait_warp(k_free(buf), (uses[buf] - 1) & 1);
+      raw_store<KB, D>(rk, sma + S::K + buf * S::OPND, 16 * grp, lane, magic);
+      if (lane == 0) s_dead[buf][uses[buf] & 1][grp] = (uint16_t)(0xffffu << live);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) arrive(v_full(x));
-      ++uses[x];
-      if (more) load_bits<D>(rv, A.c, 1, row, lane, live);
+      if (lane == 0) arrive(k_full(buf));
+      if (have1) raw_load<KB, D>(rk, kc, ks, row1, lane, live1);
+      if (uses[buf]) wait_warp(v_free(buf), (uses[buf] - 1) & 1);
+      raw_store<VB, D>(rv, sma + S::V + buf * S::OPND, 16 * grp, lane, magic);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive(v_full(buf));
+      ++uses[buf];
+      if (!have1) break;
+      raw_load<VB, D>(rv, vc, vs, row1, lane, live1);
+      row = row1;
+      live = live1;
+      buf = buf1;
+      have1 = jobs.w < jobs.w1;
+      if (have1) resolve(row1, live1, buf1);
     }
   } else {
     // ================= softmax warpgroups =================
-    const int x = warp >> 2, q4 = warp & 3, trow = 32 * q4 + lane;      // group, TMEM lanes, row of the tile
+    const int x = warp >> 2, q4 = warp & 3, trow = 32 * q4 + lane;      // group, TMEM lanes, its row
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
     const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + lanes;
+    const uint32_t qt = sma + (PAIR && x ? S::Q2 : S::Q);
     const bool plain = A.cap == 0.f, biased = A.slopes != nullptr;
     const bool issuer = (tid & 127) == 0;
-    const uint32_t id_s = idesc(128, false), id_o = idesc(D, true);
-    uint32_t uses = 0;                         // tiles of this group so far
-    auto issue_scores = [&]() {                // next S = Q K^T of this group; its tile is use number `uses`
-      if (!wait(k_full(x), uses & 1)) return;
+    constexpr uint32_t id_s = idesc(128, false), id_o = idesc(D, true);
+    uint32_t mine = 0;                         // tiles of this group so far
+    uint32_t seen_of[2] = {0u, 0u};            // uses of the buffers so far
+    // S = Q K^T of this group with the K of buffer i
+    auto issue_scores = [&](int i) {
+      if (!wait(k_full(i), seen_of[i] & 1)) return;
       umma::fence_after_sync();
-      const uint32_t kt = sma + S::K + x * S::OPND;
+      const uint32_t kt = sma + S::K + i * S::OPND;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t off = (k / 4) * BOX + (k % 4) * 32;
-        mma_ss(tmem + 128 * x, umma::smem_desc(sma + S::Q + off, 16, 1024), umma::smem_desc(kt + off, 16, 1024), id_s,
-               k != 0);
+        mma_ss(tmem + 128 * x, umma::smem_desc(qt + off, 16, 1024), umma::smem_desc(kt + off, 16, 1024), id_s, k != 0);
       }
       umma::mma_commit(s_done(x));
+      umma::mma_commit(k_free(i));
     };
     for (; jobs.w < jobs.w1; jobs.next(A)) {
-      const Seq& s = jobs.s;
+      const Seq<ROWS>& s = jobs.s;
       const int old = s.len - s.n, R = s.n * A.G, count = jobs.u1 - jobs.u0;
-      const int row = jobs.rt * ROWS + trow;
+      const int first_row = jobs.rt * ROWS + (PAIR ? 128 * x : 0), row = first_row + trow;
       const bool is = row < R;
       const int i = is ? row / A.G : 0, jq = jobs.h * A.G + (is ? row % A.G : 0);
       float down;
-      // ---- Q: row trow, half x of its features, scaled to the top of fp16's range ----
+      // ---- Q: scaled to the top of fp16's range; without PAIR each group lays out half of the features ----
       {
+        constexpr int PART = PAIR ? D : D / 2;
+        const int f0 = PAIR ? 0 : x * (D / 2);
         float mx = 0.f;
-        const long long at = (s.row0 + i) * A.q_row + jq * A.q_head + x * (D / 2);
-        const bool vec = A.q_vec;
-        for (int k = 0; k < D / 32; ++k) {
-          float v[16];
+        const long long at = (s.row0 + i) * A.q_row + jq * A.q_head + f0;
+        auto load = [&](int k, float (&v)[16]) {
           if (!is) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = 0.f;
-          } else if (A.q_f16) load_n(reinterpret_cast<const __half*>(A.q) + at + 16 * k, vec, v);
-          else load_n(reinterpret_cast<const bf16*>(A.q) + at + 16 * k, vec, v);
+          } else if (A.q_f16) {
+            load_n(reinterpret_cast<const __half*>(A.q) + at + 16 * k, A.q_vec, v);
+          } else {
+            load_n(reinterpret_cast<const bf16*>(A.q) + at + 16 * k, A.q_vec, v);
+          }
+        };
+#pragma unroll 1
+        for (int k = 0; k < PART / 16; ++k) {
+          float v[16];
+          load(k, v);
 #pragma unroll
           for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[e]));
         }
-        s_max[128 * x + trow] = mx;
-        bar_sync(3, 256);                      // and: the previous job's Q and sums are read
-        mx = fmaxf(s_max[trow], s_max[128 + trow]);
+        if constexpr (!PAIR) {
+          s_max[0][x][trow] = mx;
+          bar_sync(3, 256);
+          mx = fmaxf(s_max[0][0][trow], s_max[0][1][trow]);
+        }
         int e2 = 13;
         if (mx > 0.f && mx < INFINITY) e2 = max(ilogbf(mx), -100);
         const float up = ldexpf(1.f, 13 - e2);
         down = ldexpf(1.f, e2 - 13);
-        for (int k = 0; k < D / 32; ++k) {
+#pragma unroll 1
+        for (int k = 0; k < PART / 16; ++k) {
           float v[16];
-          if (!is) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0.f;
-          } else if (A.q_f16) load_n(reinterpret_cast<const __half*>(A.q) + at + 16 * k, vec, v);
-          else load_n(reinterpret_cast<const bf16*>(A.q) + at + 16 * k, vec, v);
+          load(k, v);
           uint32_t h[8];
-          const int bk = A.c.bits[0];
+          // places 2 e and 2 e + 1 of 16 features
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            // places 2 e and 2 e + 1 of 16 features (feature_at, for each packing)
-            const float a4 = v[(e / 4) * 8 + (e & 3)], b4 = v[(e / 4) * 8 + (e & 3) + 4];
-            const float a8 = v[(e / 2) * 4 + (e & 1)], b8 = v[(e / 2) * 4 + (e & 1) + 2];
-            const float a = bk == 4 ? a4 : bk == 8 ? a8 : v[e], b = bk == 4 ? b4 : bk == 8 ? b8 : v[e + 8];
-            h[e] = ca::h2u(__floats2half2_rn(a * up, b * up));
-          }
-          const int piece = x * (D / 16) + 2 * k;
-          sts128(piece_addr(sma + S::Q, trow, piece), h[0], h[1], h[2], h[3]);
-          sts128(piece_addr(sma + S::Q, trow, piece + 1), h[4], h[5], h[6], h[7]);
+          for (int e = 0; e < 8; ++e)
+            h[e] = ca::h2u(__floats2half2_rn(v[feature_at(KB, 2 * e)] * up, v[feature_at(KB, 2 * e + 1)] * up));
+          const int piece = f0 / 8 + 2 * k;
+          sts128(piece_addr(qt, trow, piece), h[0], h[1], h[2], h[3]);
+          sts128(piece_addr(qt, trow, piece + 1), h[4], h[5], h[6], h[7]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      bar_sync(3, 256);
+      if constexpr (PAIR) bar_sync(1 + x, 128);
+      else bar_sync(3, 256);
       const float mult = A.scale * 2.f * down * (plain ? cs::LOG2E : 1.f);      // two: the operands are halves
       const float slope = is && biased ? A.slopes[jq] * cs::LOG2E : 0.f;
       const int pq = A.positions ? A.positions[s.row0 + i] : old + i;
-      // keys before `sure` and from `edge` on are seen by every row of the tile
-      const int i0 = jobs.rt * ROWS / A.G;
-      const int sure = s.causal && !(A.window && A.positions) ? old + min(s.n, i0 + 1) : old;
+      // keys before `sure` and from `edge` on are seen by every row of the group
+      const int i0 = min(first_row / A.G, s.n - 1);
+      const int sure = s.causal && !(A.window && A.positions) ? old + i0 + 1 : old;
       int edge = 0;
       if (A.window) {
         int top = old + s.n;
         if (A.positions) {
           top = old;
-          for (int k = i0; k <= min(s.n - 1, (jobs.rt * ROWS + ROWS - 1) / A.G); ++k)
-            top = max(top, A.positions[s.row0 + k]);
+          for (int k = i0; k <= min(s.n - 1, (first_row + 127) / A.G); ++k) top = max(top, A.positions[s.row0 + k]);
         }
         edge = top - A.window + 1;
       }
-      float m_ref = -INFINITY, l = 0.f;
-      const int mine = (count - x + 1) / 2;    // tiles x, x + 2, ... of the part
-      if (issuer && mine > 0) issue_scores();
-      for (int k = 0; k < mine; ++k, ++uses) {
-        const int t0 = s.first + (jobs.u0 + 2 * k + x) * TILE;
-        wait_warp(s_done(x), uses & 1);        // S is there, and `dead`, written before the K tile was
+      float m_ref = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      const int tiles = PAIR ? count : (count - x + 1) / 2;     // of this group in this part
+      if (issuer && tiles > 0) issue_scores(PAIR ? 0 : x);
+      for (int k = 0; k < tiles; ++k, ++mine) {
+        const int jt = PAIR ? k : 2 * k + x, i_buf = jt & 1;
+        const int t0 = s.first + (jobs.u0 + jt) * TILE;
+        wait_warp(s_done(x), mine & 1);        // S is there, and s_dead, written before the K tile was
         umma::fence_after_sync();
-        const volatile uint32_t* dd = reinterpret_cast<const volatile uint32_t*>(dead + (2 * x + (uses & 1)) * 8);
-        const uint32_t d4[4] = {dd[0], dd[1], dd[2], dd[3]};
-        const bool hidden = (d4[0] | d4[1] | d4[2] | d4[3]) != 0u || t0 + TILE > sure || t0 < edge;
+        const volatile uint32_t* dd = reinterpret_cast<const volatile uint32_t*>(s_dead[i_buf][seen_of[i_buf] & 1]);
+        const uint32_t any_dead = dd[0] | dd[1] | dd[2] | dd[3];
+        const bool hidden = any_dead != 0u || t0 + TILE > sure || t0 < edge;
         const bool special = hidden || biased || !plain;
         float mx = -INFINITY;
         if (!special) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            float v[32];
-            umma::tmem_ld32(ts + c0, v);
+          for (int c0 = 0; c0 < 128; c0 += 64) {
+            uint32_t a[32], b[32];
+            tmem_ld32_async(ts + c0, a);
+            tmem_ld32_async(ts + c0 + 32, b);
+            tmem_wait_ld(a, b);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, v[e]);
+            for (int e = 0; e < 32; ++e)
+              m4[e & 3] = fmaxf(m4[e & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(b[e])));
           }
-          mx *= mult;
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * mult;
         } else {
           // capped, biased and masked scores in base 2, written back
 #pragma unroll 1
@@ -524,7 +658,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
             umma::tmem_ld32(ts + c0, v);
             uint32_t seen = 0xffffffffu;
             if (hidden) {
-              seen = ~d4[c0 / 32];
+              seen = ~dd[c0 / 32];
               const int t = t0 + c0;           // bit e: key t + e
               if (A.window) {
                 // keys in the sequence at positions above pq - window; new rows below
@@ -554,18 +688,22 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
               }
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float y = v[e] * mult;
-              if (!plain) y = cap_score(y, A.cap) * cs::LOG2E;
-              v[e] = y;
+            for (int e = 0; e < 32; ++e) v[e] *= mult;
+            if (!plain) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = cap_score(v[e], A.cap) * cs::LOG2E;
             }
             if (biased) {
-              const bool by_place = !A.positions || t0 + c0 + 32 <= old;
+              if (!A.positions || t0 + c0 + 32 <= old) {
+                const float base = (float)(pq - t0 - c0);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int t = t0 + c0 + e;
-                const int pk = by_place ? t : (t < s.len ? key_position(A, s.row0, old, t) : 0);
-                v[e] = fmaf(-slope, (float)(pq - pk), v[e]);
+                for (int e = 0; e < 32; ++e) v[e] = fmaf(-slope, base - (float)e, v[e]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const int t = t0 + c0 + e, pk = t < s.len ? key_position(A, s.row0, old, t) : 0;
+                  v[e] = fmaf(-slope, (float)(pq - pk), v[e]);
+                }
               }
             }
             if (hidden) {
@@ -574,6 +712,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
             }
 #pragma unroll
             for (int e = 0; e < 32; ++e) mx = fmaxf(mx, v[e]);
+            __syncwarp();
             tmem_st32(ts + c0, v);
           }
           tmem_wait_st();
@@ -584,9 +723,10 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
         if (__any_sync(0xffffffffu, grow)) {
           const float to_m = fmaxf(mx, m_ref), f = m_ref == -INFINITY ? 0.f : cs::ex2(m_ref - to_m);
           m_ref = to_m;
-          l *= f;
+          l2.x *= f;
+          l2.y *= f;
           if (k > 0) {
-            wait_warp(o_done(x), (uses - 1) & 1);
+            wait_warp(o_done(x), (mine - 1) & 1);
             umma::fence_after_sync();
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -600,79 +740,95 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
           }
         }
         const float ref = m_ref == -INFINITY ? 0.f : cs::SHIFT - m_ref;
+        const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(ref, ref);
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          float v[32];
-          umma::tmem_ld32(ts + c0, v);
-          uint32_t h[16];
-          float a0 = 0.f, a1 = 0.f;
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+          uint32_t a[32], b[32], h[32];
+          tmem_ld32_async(ts + c0, a);
+          tmem_ld32_async(ts + c0 + 32, b);
+          tmem_wait_ld(a, b);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p0 = cs::ex2(fmaf(v[2 * e], mul, ref)), p1 = cs::ex2(fmaf(v[2 * e + 1], mul, ref));
-            a0 += p0;
-            a1 += p1;
-            h[e] = ca::h2u(__floats2half2_rn(p0, p1));
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* v = e < 16 ? a + 2 * e : b + 2 * (e - 16);
+            const float2 z = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), mul2, ref2);
+            const float2 p = make_float2(cs::ex2(z.x), cs::ex2(z.y));
+            l2 = __fadd2_rn(l2, p);
+            h[e] = ca::h2u(__floats2half2_rn(p.x, p.y));
           }
-          l += a0 + a1;
-          tmem_st16(ts + c0 / 2, h);
+          tmem_st32u(ts + c0 / 2, h);
         }
         tmem_wait_st();
         umma::fence_before_sync();
         bar_sync(1 + x, 128);
+        const uint32_t use = seen_of[i_buf]++;
         if (issuer) {
           umma::fence_after_sync();
-          if (wait(v_full(x), uses & 1)) {
+          if (wait(v_full(i_buf), use & 1)) {
             umma::fence_after_sync();
-            const uint32_t vt = sma + S::V + x * S::OPND;
+            const uint32_t vt = sma + S::V + i_buf * S::OPND;
 #pragma unroll
             for (int kk = 0; kk < TILE / 16; ++kk)
               mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, umma::smem_desc(vt + kk * 2048, BOX, 1024), id_o,
                      (k | kk) != 0);
             umma::mma_commit(o_done(x));
+            umma::mma_commit(v_free(i_buf));
           }
-          if (k + 1 < mine) {
-            ++uses;
-            issue_scores();
-            --uses;
-          }
+          if (k + 1 < tiles) issue_scores(PAIR ? i_buf ^ 1 : i_buf);
         }
       }
-      // ---- the two groups' sums joined, half of the features by each ----
-      if (mine > 0) wait_warp(o_done(x), (uses - 1) & 1);
-      s_ml[2 * (128 * x + trow)] = m_ref;
-      s_ml[2 * (128 * x + trow) + 1] = l;
-      umma::fence_before_sync();
-      bar_sync(3, 256);
-      umma::fence_after_sync();
-      const float m0 = s_ml[2 * trow], l0 = s_ml[2 * trow + 1], m1 = s_ml[2 * (128 + trow)], l1 = s_ml[2 * (128 + trow) + 1];
-      const float top = fmaxf(m0, m1);
-      const float f0 = l0 == 0.f ? 0.f : cs::ex2(m0 - top), f1 = l1 == 0.f ? 0.f : cs::ex2(m1 - top);
-      const float sum = l0 * f0 + l1 * f1;
-      const bool whole = jobs.u0 == 0 && jobs.u1 == jobs.units, two = count > 1;
-      float* rec = A.pieces + ((2ll * blockIdx.x + (jobs.u0 == 0 ? 1 : 0)) * ROWS + trow) * (D + 4);
+      if (tiles > 0) wait_warp(o_done(x), (mine - 1) & 1);
+      const bool whole = jobs.u0 == 0 && jobs.u1 == jobs.units;
+      const float l = l2.x + l2.y;
       const uint32_t o0 = tmem + 256 + lanes, o1 = o0 + 128;
+      float f0 = 2.f, f1 = 0.f, top = m_ref, sum = l;        // two: the operands are halves
+      int cb = 0, ce = D;
+      if constexpr (!PAIR) {
+        // the two groups' sums joined, half of the features by each
+        s_ml[x][trow] = make_float2(m_ref, l);
+        umma::fence_before_sync();
+        bar_sync(3, 256);
+        umma::fence_after_sync();
+        const float2 g0 = s_ml[0][trow], g1 = s_ml[1][trow];
+        top = fmaxf(g0.x, g1.x);
+        f0 = g0.y == 0.f ? 0.f : 2.f * cs::ex2(g0.x - top);
+        f1 = g1.y == 0.f ? 0.f : 2.f * cs::ex2(g1.x - top);
+        sum = 0.5f * (g0.y * f0 + g1.y * f1);
+        cb = x * (D / 2);
+        ce = cb + D / 2;
+      } else {
+        umma::fence_after_sync();
+      }
+      float* rec = A.pieces + ((2ll * blockIdx.x + (jobs.u0 == 0 ? 1 : 0)) * ROWS + (row - jobs.rt * ROWS)) * (D + 4);
 #pragma unroll 1
-      for (int c0 = x * (D / 2); c0 < (x + 1) * (D / 2); c0 += 32) {
-        float v[32], v1[32];
+      for (int c0 = cb; c0 < ce; c0 += 32) {
+        float v[32];
         __syncwarp();
-        umma::tmem_ld32(o0 + c0, v);
-        if (two) umma::tmem_ld32(o1 + c0, v1);
+        umma::tmem_ld32((PAIR && x ? o1 : o0) + c0, v);
+        if constexpr (PAIR) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float y = f0 != 0.f ? 2.f * f0 * v[e] : 0.f;       // two: the operands are halves
-          if (two && f1 != 0.f) y = fmaf(2.f * f1, v1[e], y);
-          v[e] = y;
+          for (int e = 0; e < 32; ++e) v[e] = sum != 0.f ? 2.f * v[e] : 0.f;
+        } else {
+          float v1[32];
+          if (count > 1) umma::tmem_ld32(o1 + c0, v1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float y = f0 != 0.f ? f0 * v[e] : 0.f;
+            v[e] = count > 1 && f1 != 0.f ? fmaf(f1, v1[e], y) : y;
+          }
         }
         if (!is) continue;
-        const int bv = A.c.bits[1];
+        if (whole) {
+          store_places<D, VB>(A, s.row0 + i, jq, c0, v, sum, top);
+        } else {
+          float y[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int d = feature_at(bv, c0 + e);
-          if (whole) store_out(A, D, s.row0 + i, jq, d, v[e], sum, top);
-          else rec[d] = v[e];
+          for (int e = 0; e < 32; ++e) y[feature_at(VB, e)] = v[e];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(rec + c0 + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
         }
       }
-      if (!whole && is && x == 0) {
+      if (!whole && is && (PAIR || x == 0)) {
         rec[D] = top;
         rec[D + 1] = sum;
       }
@@ -680,13 +836,15 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
         A.notes[blockIdx.x] = make_int4(
             jobs.b, jobs.h, jobs.rt, cs::pieces_until(total, parts, blockIdx.x, jobs.base + jobs.units));
       }
+      // O is read and Q no longer needed before the next job's first product
       umma::fence_before_sync();
-      bar_sync(3, 256);     // O is read before the next job's first product writes it
+      if constexpr (PAIR) bar_sync(1 + x, 128);
+      else bar_sync(3, 256);
       umma::fence_after_sync();
     }
     if (issuer) {
       umma::mma_commit(drain(x));
-      if (!umma::mbar_wait(drain(x), 0)) *abort_flag = 1;
+      if (!ct::mbar_wait(drain(x), 0)) *abort_flag = 1;
       if (*abort_flag) raise_status(A.a.status, DEV_ERR_TIMEOUT);
     }
   }

@@ -1,9 +1,10 @@
 // Launch of the cache attention kernels: which kernel takes how many rows, how many blocks, and
-// the join behind it.  The narrow kernel's instances for every pair of bit-widths are compiled in
-// sources of their own (cache_few_d64.cu, cache_few_d128.cu), beside one another.
+// the join behind it.  The kernels' instances for every pair of bit-widths are compiled in
+// sources of their own, beside one another.
 #pragma once
 
 #include "cache_attend.cuh"
+#include "cache_attend_tc.cuh"
 #include "host.cuh"
 
 namespace jolt {
@@ -29,13 +30,14 @@ inline int few_blocks(const CacheArgs& c, int nt) {
   return 148 * (by_regs < by_smem ? by_regs : by_smem);
 }
 
-// launch with programmatic stream serialization: the join's blocks may be scheduled while the
-// last blocks of the kernel before it run; they wait for its end before they read
+// launch with programmatic stream serialization: the blocks may be brought up while the kernel
+// before them in the stream ends; every thread waits for that end before it reads or writes
 template <typename K>
-cudaError_t launch_after(K kernel, dim3 grid, int threads, const CacheAttendArgs& A, cudaStream_t st) {
+cudaError_t launch_after(K kernel, dim3 grid, int threads, size_t smem, const CacheAttendArgs& A, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -51,10 +53,33 @@ template <int D, int NT, int KB, int VB>
 jolt_status launch_few(const CacheAttendArgs& A, cudaStream_t st) {
   const int smem = ca::Smem<D, NT>::bytes(KB, VB), blocks = few_blocks(A.c, NT);
   CUDA_TRY(cudaFuncSetAttribute(cache_few_rows_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  count_launch(), cache_few_rows_kernel<D, NT, KB, VB><<<blocks, ca::WARPS * 32, smem, st>>>(A);
-  CUDA_TRY(cudaGetLastError());
-  CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT, 1, 256 / D>, dim3(blocks, A.a.max_new * A.G), 256, A, st));
+  CUDA_TRY(launch_after(cache_few_rows_kernel<D, NT, KB, VB>, dim3(blocks), ca::WARPS * 32, smem, A, st));
+  CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT, 1, 256 / D>, dim3(blocks, A.a.max_new * A.G), 256, 0, A, st));
   return JOLT_OK;
+}
+
+template <int D, int KB, int VB, bool PAIR>
+jolt_status launch_many(const CacheAttendArgs& A, cudaStream_t st) {
+  constexpr int smem = ct::Smem<D>::bytes(PAIR), rows = PAIR ? 256 : 128;
+  CUDA_TRY(cudaFuncSetAttribute(cache_many_rows_kernel<D, KB, VB, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  CUDA_TRY(launch_after(cache_many_rows_kernel<D, KB, VB, PAIR>, dim3(MANY_BLOCKS), ct::THREADS, smem, A, st));
+  CUDA_TRY(launch_after(cache_join_kernel<D, rows, 8, 1>, dim3(MANY_BLOCKS, rows / 8), 256, 0, A, st));
+  return JOLT_OK;
+}
+
+template <int D, bool PAIR>
+jolt_status launch_many_bits(const CacheAttendArgs& A, cudaStream_t st) {
+  switch (A.c.bits[0] * 16 + A.c.bits[1]) {
+    case 0x22: return launch_many<D, 2, 2, PAIR>(A, st);
+    case 0x24: return launch_many<D, 2, 4, PAIR>(A, st);
+    case 0x28: return launch_many<D, 2, 8, PAIR>(A, st);
+    case 0x42: return launch_many<D, 4, 2, PAIR>(A, st);
+    case 0x44: return launch_many<D, 4, 4, PAIR>(A, st);
+    case 0x48: return launch_many<D, 4, 8, PAIR>(A, st);
+    case 0x82: return launch_many<D, 8, 2, PAIR>(A, st);
+    case 0x84: return launch_many<D, 8, 4, PAIR>(A, st);
+    default: return launch_many<D, 8, 8, PAIR>(A, st);
+  }
 }
 
 template <int D, int NT>
@@ -75,5 +100,9 @@ jolt_status launch_few_bits(const CacheAttendArgs& A, cudaStream_t st) {
 // the narrow kernel with nt n-tiles, and its join
 template <int D>
 jolt_status launch_few_rows(const CacheAttendArgs& A, int nt, cudaStream_t st);
+
+// the tensor-core kernel with jobs of 128 rows or (pair) 256, and its join
+template <int D>
+jolt_status launch_many_rows(const CacheAttendArgs& A, bool pair, cudaStream_t st);
 
 }  // namespace jolt

@@ -31,7 +31,7 @@ struct CacheAttendArgs {
   long long q_row, q_head;
   void* out;
   long long o_row, o_head;
-  bool q_vec;                // rows and heads of q are 16-byte aligned
+  bool q_vec, o_vec;         // rows and heads of q and of the output are 16-byte aligned
   // scratch
   int4* notes;               // [blocks]: {sequence, KV head, row tile or -1, blocks with a piece}
   float* pieces;             // [blocks][2][rows of a tile][D + 4]: D outputs, maximum, sum
@@ -50,6 +50,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// Programmatic launch: the kernel before this one in its stream has ended and its writes are seen.
+// (A kernel launched so may start while that one ends; the waiting is all that keeps them apart.)
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// the next kernel's blocks may be brought up from here on, to wait for this one's end
+__device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // start of block c's range when `total` units are dealt to `parts` blocks
 __device__ __forceinline__ long long range_start(long long total, int parts, int c) { return total * c / parts; }
@@ -116,7 +122,7 @@ __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendArgs A) {
   constexpr int REC = D + 4, MOST = 592, AT_ONCE = 256 / (D * GROUPS);
   __shared__ float2 ml[AT_ONCE][MOST];      // maximum and sum of every piece
   __shared__ float part[AT_ONCE][GROUPS][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  cs::wait_for_predecessor();
   const int c0 = blockIdx.x, tid = threadIdx.x;
   const int4 note = A.notes[c0];
   const int b = note.x, h = note.y, tile = note.z, count = note.w;

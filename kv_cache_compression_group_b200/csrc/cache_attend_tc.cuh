@@ -2,20 +2,22 @@
 // 5th-generation tensor cores.
 //
 // A job is 128 rows (new row x query head) of one KV head, or 256 where there are more; its keys come
-// in tiles of 128 tokens.  One persistent CTA of 16 warps per SM:
+// in tiles of 128 tokens.  One persistent CTA of 20 warps per SM:
+//   * one warp walks the tiles and looks up their pages, several tiles ahead;
 //   * eight dequantising warps take 16 tokens of every tile each: packed codes and (lo, step) pairs
-//     straight to registers, one tile ahead (and the page's number two), then
-//     fp16(lo / 2 + code * (step / 2)) into the 128-byte-swizzled operand tiles, two of K and two of V.
-//     The features of a row keep the order in which a packed word gives its pairs; Q is laid out in
-//     the same order, the output columns are put back.
+//     straight to registers, one tile ahead, then fp16(lo / 2 + code * (step / 2)) into the
+//     128-byte-swizzled operand tiles, two of K and two of V.  The features of a row keep the order
+//     in which a packed word gives its pairs; Q is laid out in the same order, the output columns
+//     are put back;
 //   * two softmax warpgroups with score and output accumulators of their own (all 512 columns of
-//     tensor memory), so that one group's exponentials overlap the other's products.  With 256 rows
-//     each has 128 of them and both use every tile, which halves the dequantisation; with 128 rows
-//     one takes the even and the other the odd tiles, joined at the end.  A thread has one row: it
-//     reads its scores twice (maximum, then weights), writes the weights as fp16 over the scores, and
-//     when its group has, one elected thread issues O += P V (P from tensor memory) and the group's
-//     next S = Q K^T.  The reference maximum may lag by 2^8, so rescaling O, a pass through tensor
-//     memory, is rare after the first tiles.
+//     tensor memory).  With 256 rows each has 128 of them and both use every tile, which halves the
+//     dequantisation; with 128 rows one takes the even and the other the odd tiles, joined at the
+//     end.  A thread has one row and takes 64 keys at a time: scores to registers, maximum, weights,
+//     and these as fp16 over the scores.  The reference maximum may lag by 2^8, so rescaling O, a
+//     pass through tensor memory, is rare after the first tiles;
+//   * one warp issues the products.  A group's scores lie in two halves of 64 keys: while its warps
+//     are at the one, O += P V (P from tensor memory) and the next tile's S = Q K^T of the other run.
+//     (With whole tiles, a group waited for its own products: 4600 cycles per tile instead.)
 // What bounds it at D = 128: the two products take 1024 cycles per 128 x 128 tile, its 16384
 // exponentials 1024 at 16 per cycle, and the instructions of softmax (about 450 per scheduler) and
 // of dequantisation (about 600, once per 256 rows) come next to them.
@@ -30,7 +32,8 @@
 namespace jolt {
 namespace ct {
 constexpr int TILE = 128;
-constexpr int THREADS = 512;
+constexpr int THREADS = 640;
+constexpr int RING = 8;                        // tiles that the walk is ahead
 constexpr int BOX = 128 * 128;                 // bytes of 128 rows x 64 fp16 features
 template <int D>
 struct Smem {
@@ -54,15 +57,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
       ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
-        "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
-        "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]),
-        "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(taddr)
+        "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -136,6 +146,26 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[3
         "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
         "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+// Registers of a thread of each role.  640 threads are launched with 96, 61440 in all, which the shares
+// 256 x 120 + 256 x 88 + 128 x 64 use up.
+constexpr int SOFTMAX_REGS = 120, DEQUANT_REGS = 88, ISSUE_REGS = 64;
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // 16-byte piece `piece` (8 features) of row `row` of an operand tile
 __device__ __forceinline__ uint32_t piece_addr(uint32_t tile, int row, int piece) {
@@ -368,10 +398,11 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   constexpr int ROWS = PAIR ? 256 : 128;
   extern __shared__ unsigned char ct_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)ct_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t bars[14];
+  __shared__ __align__(8) uint64_t bars[21 + 2 * RING];
   __shared__ uint32_t tmem_slot;
   __shared__ int aborted, s_b;
-  __shared__ long long s_sum[16], s_base;
+  __shared__ long long s_sum[THREADS / 32], s_base;
+  __shared__ longlong2 s_ring[RING][8];                   // {first row in the pool, or -1 for the end; buffer, tokens}
   __shared__ __align__(16) uint16_t s_dead[2][2][8];      // [buffer][parity of its use][16 tokens each]
   __shared__ float s_max[2][2][128];                      // largest |q| of [group][half of the features][row]
   __shared__ float2 s_ml[2][128];                         // maximum and sum of [group][row]
@@ -379,14 +410,18 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sma = umma::smem_u32(sm), bar0 = umma::smem_u32(bars);
   // barriers of buffer i: K written, K no longer needed, V written, V no longer needed; of group x:
-  // S = Q K^T done, O += P V done, all done
+  // Q laid out; of its half h: S = Q K^T done, P written, O += P V done; all products done; of the ring
   auto k_full = [&](int i) { return bar0 + 8 * i; };
   auto k_free = [&](int i) { return bar0 + 16 + 8 * i; };
   auto v_full = [&](int i) { return bar0 + 32 + 8 * i; };
   auto v_free = [&](int i) { return bar0 + 48 + 8 * i; };
-  auto s_done = [&](int x) { return bar0 + 64 + 8 * x; };
-  auto o_done = [&](int x) { return bar0 + 80 + 8 * x; };
-  auto drain = [&](int x) { return bar0 + 96 + 8 * x; };
+  auto s_done = [&](int x, int h) { return bar0 + 64 + 16 * x + 8 * h; };
+  auto p_full = [&](int x, int h) { return bar0 + 96 + 16 * x + 8 * h; };
+  auto q_full = [&](int x) { return bar0 + 128 + 8 * x; };
+  auto o_done = [&](int x) { return bar0 + 144 + 8 * x; };   // (of one half, then of the other)
+  auto ring_full = [&](int i) { return bar0 + 160 + 8 * i; };
+  auto ring_free = [&](int i) { return bar0 + 160 + 8 * (RING + i); };
+  const uint32_t drained = bar0 + 160 + 16 * RING;
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (*abort_flag) return false;
     if (ct::mbar_wait(bar, parity)) return true;
@@ -401,13 +436,21 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       umma::mbar_init(k_full(i), 8);
-      umma::mbar_init(k_free(i), PAIR ? 2 : 1);
+      umma::mbar_init(k_free(i), 1);
       umma::mbar_init(v_full(i), 8);
-      umma::mbar_init(v_free(i), PAIR ? 2 : 1);
-      umma::mbar_init(s_done(i), 1);
+      umma::mbar_init(v_free(i), 1);
+      for (int h = 0; h < 2; ++h) {
+        umma::mbar_init(s_done(i, h), 1);
+        umma::mbar_init(p_full(i, h), 4);
+      }
+      umma::mbar_init(q_full(i), PAIR ? 4 : 8);
       umma::mbar_init(o_done(i), 1);
-      umma::mbar_init(drain(i), 1);
     }
+    for (int i = 0; i < RING; ++i) {
+      umma::mbar_init(ring_full(i), 1);
+      umma::mbar_init(ring_free(i), 8);
+    }
+    umma::mbar_init(drained, 1);
     aborted = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -423,7 +466,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   if (lane == 0) s_sum[warp] = total;
   __syncthreads();
   total = 0;
-  for (int k = 0; k < 16; ++k) total += s_sum[k];
+  for (int k = 0; k < THREADS / 32; ++k) total += s_sum[k];
   const int parts = (int)min((long long)gridDim.x, total);
   if ((int)blockIdx.x >= parts) return;   // the whole block
   const long long w0 = cs::range_start(total, parts, blockIdx.x), w1 = cs::range_start(total, parts, blockIdx.x + 1);
@@ -460,98 +503,189 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   Jobs<ROWS> jobs;
   jobs.start(A, w0, w1, s_b, s_base);
 
-  if (warp >= 8) {
+  if (warp >= 16) {
+    regs_down<ISSUE_REGS>();
+    if (warp == 17) {
+      // ================= the walk over the tiles =================
+      // lanes 0 .. 7: 16 tokens each
+      int slot = 0;
+      uint32_t round = 0;
+      auto publish = [&](long long row, int buf, int live) {
+        if (round > 0) wait_warp(ring_free(slot), (round - 1) & 1);
+        if (lane < 8) s_ring[slot][lane] = make_longlong2(row, (long long)buf << 32 | (unsigned)live);
+        __syncwarp();
+        if (lane == 0) arrive(ring_full(slot));
+        if (++slot == RING) {
+          slot = 0;
+          ++round;
+        }
+      };
+      for (; jobs.w < jobs.w1; jobs.next(A))
+        for (int tile = jobs.u0; tile < jobs.u1; ++tile) {
+          const int t = jobs.s.first + tile * TILE + 16 * (lane & 7);
+          long long row = 0;
+          int live = 0;
+          if (t < jobs.s.len) {
+            const int page = page_at(A.a, A.c, jobs.b, t);
+            if (page >= 0) {
+              row = row_index(A.c, page, jobs.h, t);
+              live = min(16, jobs.s.len - t);
+            }
+          }
+          __syncwarp();
+          publish(row, (tile - jobs.u0) & 1, live);
+        }
+      publish(-1, 0, 0);
+    } else if (warp == 16) {
+      // ================= the products =================
+      constexpr uint32_t id_s = idesc(64, false), id_o = idesc(D, true);
+      const uint64_t kd = umma::smem_desc(sma + S::K, 16, 1024), vd = umma::smem_desc(sma + S::V, BOX, 1024);
+      uint32_t k_uses[2] = {0u, 0u}, v_uses[2] = {0u, 0u}, done[2] = {0u, 0u}, round = 0;
+      auto going = [&]() { return !__any_sync(0xffffffffu, *abort_flag); };
+      // S = Q K^T of group x, half hf of the keys of buffer i; `last`: nobody else needs K after it
+      auto scores_of = [&](int x, int hf, int i, bool last) {
+        wait_warp(k_full(i), k_uses[i] & 1);
+        umma::fence_after_sync();
+        const uint64_t qd = umma::smem_desc(sma + (PAIR && x ? S::Q2 : S::Q), 16, 1024);
+        const uint64_t kh = kd + (uint64_t)((i * S::OPND + hf * 64 * 128) >> 4);
+        if (going() && elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (uint64_t)(((k / 4) * BOX + (k % 4) * 32) >> 4);
+            mma_ss(tmem + 128 * x + 64 * hf, qd + off, kh + off, id_s, k != 0);
+          }
+          umma::mma_commit(s_done(x, hf));
+          if (last) umma::mma_commit(k_free(i));
+        }
+        __syncwarp();
+        if (last) ++k_uses[i];
+      };
+      for (; jobs.w < jobs.w1; jobs.next(A), ++round) {
+        const int count = jobs.u1 - jobs.u0;
+        for (int x = 0; x < 2; ++x) {
+          wait_warp(q_full(PAIR ? x : 0), round & 1);
+          if (PAIR || x < count)
+            for (int hf = 0; hf < 2; ++hf) scores_of(x, hf, PAIR ? 0 : x, hf == 1 && (!PAIR || x == 1));
+        }
+        for (int k = 0; k < (PAIR ? count : (count + 1) / 2); ++k) {
+          for (int hf = 0; hf < 2; ++hf) {
+            for (int x = 0; x < 2; ++x) {
+              const int jt = PAIR ? k : 2 * k + x, i = jt & 1;
+              if (jt >= count) break;
+              wait_warp(p_full(x, hf), done[x] & 1);
+              wait_warp(v_full(i), v_uses[i] & 1);
+              umma::fence_after_sync();
+              const bool last = hf == 1 && (!PAIR || x == 1);
+              if (going() && elect_one()) {
+                const uint64_t vh = vd + (uint64_t)((i * S::OPND + hf * 64 * 128) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 64 * hf + 8 * kk, vh + (uint64_t)((kk * 2048) >> 4),
+                         id_o, (k | hf | kk) != 0);
+                umma::mma_commit(o_done(x));
+                if (last) umma::mma_commit(v_free(i));
+              }
+              __syncwarp();
+              if (last) ++v_uses[i];
+              if (hf == 1) ++done[x];
+              if (jt + (PAIR ? 1 : 2) < count) scores_of(x, hf, PAIR ? i ^ 1 : i, last);
+            }
+          }
+        }
+      }
+      if (elect_one()) umma::mma_commit(drained);
+      __syncwarp();
+      if (!ct::mbar_wait(drained, 0)) *abort_flag = 1;
+      if (*abort_flag && lane == 0) raise_status(A.a.status, DEV_ERR_TIMEOUT);
+    }
+  } else if (warp >= 8) {
     // ================= dequantising warps =================
+    regs_down<DEQUANT_REGS>();
     const int grp = warp - 8;                  // tokens 16 grp .. + 15 of every tile
     const uint32_t magic = ca::magic1024();
     const unsigned char* const kc = A.c.codes[0];
     const unsigned char* const vc = A.c.codes[1];
     const __half2* const ks = A.c.scales[0];
     const __half2* const vs = A.c.scales[1];
+    // Tiles are stored as K0 K1 V0 K2 V1 K3 V2 ...: the second group's next scores want K two tiles
+    // ahead of the values that the first group's products have yet to release.
+    struct Tile {
+      long long row;      // of the pool, or -1 behind the last tile
+      int live, buf;      // tokens that exist, buffers
+    };
     RawRegs rk, rv;
-    uint32_t uses[2] = {0u, 0u};
-    // The walk over the tiles runs ahead: `ahead` is the tile whose page number is being looked up.
-    int tile = jobs.u0, j = 0;                 // of the job; its number in this block's part
-    int num = 0;                               // page number of that tile's 16 tokens
-    auto look_up = [&]() {
-      const int t = jobs.s.first + tile * TILE + 16 * grp;
-      num = t < jobs.s.len ? A.a.table[(long long)jobs.b * A.a.max_pages + (t >> A.c.page_shift)] : -1;
+    uint32_t k_uses[2] = {0u, 0u}, v_uses[2] = {0u, 0u}, round = 0;
+    int slot = 0;
+    auto take = [&]() {                        // the next tile of the walk
+      wait_warp(ring_full(slot), round & 1);
+      const longlong2 e = s_ring[slot][grp];
+      const Tile t{__any_sync(0xffffffffu, *abort_flag) ? -1 : e.x, (int)e.y, (int)(e.y >> 32)};
+      if (lane == 0) arrive(ring_free(slot));
+      if (++slot == RING) {
+        slot = 0;
+        ++round;
+      }
+      return t;
     };
-    auto resolve = [&](long long& row, int& live, int& buf) {   // where that tile's rows are; then on to the next
-      const int t = jobs.s.first + tile * TILE + 16 * grp;
-      live = 0;
-      buf = j & 1;
-      if (t < jobs.s.len) {
-        if ((unsigned)num < (unsigned)A.c.n_pages) {
-          row = row_index(A.c, num, jobs.h, t);
-          live = min(16, jobs.s.len - t);
-        } else {
-          raise_status(A.a.status, DEV_ERR_BATCH);
+    auto load_k = [&](const Tile& t) { raw_load<KB, D>(rk, kc, ks, t.row, lane, t.live); };
+    auto load_v = [&](const Tile& t) { raw_load<VB, D>(rv, vc, vs, t.row, lane, t.live); };
+    auto store_k = [&](const Tile& t) {
+      const int i = t.buf;
+      if (k_uses[i]) wait_warp(k_free(i), (k_uses[i] - 1) & 1);
+      raw_store<KB, D>(rk, sma + S::K + i * S::OPND, 16 * grp, lane, magic);
+      if (lane == 0) s_dead[i][k_uses[i] & 1][grp] = (uint16_t)(0xffffu << t.live);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive(k_full(i));
+      ++k_uses[i];
+    };
+    auto store_v = [&](const Tile& t) {
+      const int i = t.buf;
+      if (v_uses[i]) wait_warp(v_free(i), (v_uses[i] - 1) & 1);
+      raw_store<VB, D>(rv, sma + S::V + i * S::OPND, 16 * grp, lane, magic);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive(v_full(i));
+      ++v_uses[i];
+    };
+    const Tile none{-1, 0, 0};
+    Tile e0 = take(), e1 = none, e2 = none;
+    if (e0.row >= 0) {
+      load_k(e0);
+      load_v(e0);
+      e1 = take();
+      store_k(e0);
+      if (e1.row >= 0) {
+        load_k(e1);
+        e2 = take();
+        store_k(e1);
+        if (e2.row >= 0) load_k(e2);
+      }
+      for (;;) {
+        const Tile e3 = e2.row >= 0 ? take() : none;
+        store_v(e0);
+        if (e1.row < 0) break;
+        load_v(e1);
+        if (e2.row >= 0) {
+          store_k(e2);
+          if (e3.row >= 0) load_k(e3);
         }
+        e0 = e1;
+        e1 = e2;
+        e2 = e3;
       }
-      ++tile;
-      ++j;
-      if (tile == jobs.u1) {
-        jobs.next(A);
-        tile = jobs.u0;
-        j = 0;
-      }
-      if (jobs.w < jobs.w1) look_up();
-    };
-    long long row = 0, row1 = 0;
-    int live, live1 = 0, buf, buf1 = 0;
-    look_up();
-    resolve(row, live, buf);
-    raw_load<KB, D>(rk, kc, ks, row, lane, live);
-    raw_load<VB, D>(rv, vc, vs, row, lane, live);
-    bool have1 = jobs.w < jobs.w1;             // a tile after the one in hand
-    if (have1) resolve(row1, live1, buf1);
-    for (;;) {
-      if (uses[buf]) wait_warp(k_free(buf), (uses[buf] - 1) & 1);
-      raw_store<KB, D>(rk, sma + S::K + buf * S::OPND, 16 * grp, lane, magic);
-      if (lane == 0) s_dead[buf][uses[buf] & 1][grp] = (uint16_t)(0xffffu << live);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) arrive(k_full(buf));
-      if (have1) raw_load<KB, D>(rk, kc, ks, row1, lane, live1);
-      if (uses[buf]) wait_warp(v_free(buf), (uses[buf] - 1) & 1);
-      raw_store<VB, D>(rv, sma + S::V + buf * S::OPND, 16 * grp, lane, magic);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) arrive(v_full(buf));
-      ++uses[buf];
-      if (!have1) break;
-      raw_load<VB, D>(rv, vc, vs, row1, lane, live1);
-      row = row1;
-      live = live1;
-      buf = buf1;
-      have1 = jobs.w < jobs.w1;
-      if (have1) resolve(row1, live1, buf1);
     }
   } else {
+    regs_up<SOFTMAX_REGS>();
     // ================= softmax warpgroups =================
     const int x = warp >> 2, q4 = warp & 3, trow = 32 * q4 + lane;      // group, TMEM lanes, its row
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
     const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + lanes;
     const uint32_t qt = sma + (PAIR && x ? S::Q2 : S::Q);
     const bool plain = A.cap == 0.f, biased = A.slopes != nullptr;
-    const bool issuer = (tid & 127) == 0;
-    constexpr uint32_t id_s = idesc(128, false), id_o = idesc(D, true);
     uint32_t mine = 0;                         // tiles of this group so far
     uint32_t seen_of[2] = {0u, 0u};            // uses of the buffers so far
-    // S = Q K^T of this group with the K of buffer i
-    auto issue_scores = [&](int i) {
-      if (!wait(k_full(i), seen_of[i] & 1)) return;
-      umma::fence_after_sync();
-      const uint32_t kt = sma + S::K + i * S::OPND;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t off = (k / 4) * BOX + (k % 4) * 32;
-        mma_ss(tmem + 128 * x, umma::smem_desc(qt + off, 16, 1024), umma::smem_desc(kt + off, 16, 1024), id_s, k != 0);
-      }
-      umma::mma_commit(s_done(x));
-      umma::mma_commit(k_free(i));
-    };
+    uint32_t outs = 0;                         // products O += P V so far
     for (; jobs.w < jobs.w1; jobs.next(A)) {
       const Seq<ROWS>& s = jobs.s;
       const int old = s.len - s.n, R = s.n * A.G, count = jobs.u1 - jobs.u0;
@@ -606,8 +740,8 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      if constexpr (PAIR) bar_sync(1 + x, 128);
-      else bar_sync(3, 256);
+      __syncwarp();
+      if (lane == 0) arrive(q_full(PAIR ? x : 0));
       const float mult = A.scale * 2.f * down * (plain ? cs::LOG2E : 1.f);      // two: the operands are halves
       const float slope = is && biased ? A.slopes[jq] * cs::LOG2E : 0.f;
       const int pq = A.positions ? A.positions[s.row0 + i] : old + i;
@@ -626,127 +760,109 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
       float m_ref = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       const int tiles = PAIR ? count : (count - x + 1) / 2;     // of this group in this part
-      if (issuer && tiles > 0) issue_scores(PAIR ? 0 : x);
       for (int k = 0; k < tiles; ++k, ++mine) {
         const int jt = PAIR ? k : 2 * k + x, i_buf = jt & 1;
-        const int t0 = s.first + (jobs.u0 + jt) * TILE;
-        wait_warp(s_done(x), mine & 1);        // S is there, and s_dead, written before the K tile was
-        umma::fence_after_sync();
-        const volatile uint32_t* dd = reinterpret_cast<const volatile uint32_t*>(s_dead[i_buf][seen_of[i_buf] & 1]);
-        const uint32_t any_dead = dd[0] | dd[1] | dd[2] | dd[3];
-        const bool hidden = any_dead != 0u || t0 + TILE > sure || t0 < edge;
-        const bool special = hidden || biased || !plain;
-        float mx = -INFINITY;
-        if (!special) {
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 64) {
-            uint32_t a[32], b[32];
-            tmem_ld32_async(ts + c0, a);
-            tmem_ld32_async(ts + c0 + 32, b);
-            tmem_wait_ld(a, b);
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          const int t0 = s.first + (jobs.u0 + jt) * TILE + 64 * hf;
+          const uint32_t tsh = ts + 64 * hf;
+          wait_warp(s_done(x, hf), mine & 1);    // S is there, and s_dead, written before the K tile was
+          umma::fence_after_sync();
+          const volatile uint32_t* dd =
+              reinterpret_cast<const volatile uint32_t*>(s_dead[i_buf][seen_of[i_buf] & 1]) + 2 * hf;
+          const uint32_t dead0 = dd[0], dead1 = dd[1];
+          const bool hidden = (dead0 | dead1) != 0u || t0 + 64 > sure || t0 < edge;
+          const bool special = hidden || biased || !plain;
+          uint32_t a[32], b[32];
+          tmem_ld32_async(tsh, a);
+          tmem_ld32_async(tsh + 32, b);
+          tmem_wait_ld(a, b);
+          float mx = -INFINITY;
+          if (!special) {
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               m4[e & 3] = fmaxf(m4[e & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(b[e])));
-          }
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * mult;
-        } else {
-          // capped, biased and masked scores in base 2, written back
-#pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
-            float v[32];
-            umma::tmem_ld32(ts + c0, v);
-            uint32_t seen = 0xffffffffu;
-            if (hidden) {
-              seen = ~dd[c0 / 32];
-              const int t = t0 + c0;           // bit e: key t + e
-              if (A.window) {
-                // keys in the sequence at positions above pq - window; new rows below
-                const int lowest = max(pq, old) - A.window + 1 - t;
-                const int low = A.positions ? min(lowest, max(old - t, 0)) : lowest;
-                if (low >= 32) seen = 0u;
-                else if (low > 0) seen &= 0xffffffffu << low;
-              }
-              if (t + 32 > old) {
-                const int j0 = t - old;        // new row of bit 0 (negative: earlier keys)
-                uint32_t fresh;                // bits of the new rows that the row sees
-                if (!A.mask) {
-                  const int upto = i - j0;     // bits 0 .. upto
-                  fresh = upto < 0 ? 0u : upto >= 31 ? 0xffffffffu : (2u << upto) - 1u;
-                } else {
-                  const uint32_t* words = A.mask + (long long)(s.row0 + i) * A.words;
-                  const int wi = j0 >> 5, sh = j0 & 31;
-                  const uint32_t lo = wi >= 0 && wi < A.words ? words[wi] : 0u;
-                  const uint32_t hi = wi + 1 >= 0 && wi + 1 < A.words ? words[wi + 1] : 0u;
-                  fresh = __funnelshift_r(lo, hi, sh);
+            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * mult;
+          } else {
+            // capped, biased and masked scores in base 2
+            auto special_scores = [&](uint32_t (&v)[32], int t, uint32_t dead) {   // v[e]: key t + e
+              uint32_t seen = 0xffffffffu;
+              if (hidden) {
+                seen = ~dead;
+                if (A.window) {
+                  // keys in the sequence at positions above pq - window; new rows below
+                  const int lowest = max(pq, old) - A.window + 1 - t;
+                  const int low = A.positions ? min(lowest, max(old - t, 0)) : lowest;
+                  if (low >= 32) seen = 0u;
+                  else if (low > 0) seen &= 0xffffffffu << low;
                 }
-                const uint32_t new_bits = j0 >= 0 ? 0xffffffffu : 0xffffffffu << -j0;
-                seen &= ~new_bits | fresh;
-                if (A.window && A.positions)
-                  for (int e = max(0, -j0); e < 32 && j0 + e < s.n; ++e)
-                    if (pq - A.positions[s.row0 + j0 + e] >= A.window) seen &= ~(1u << e);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= mult;
-            if (!plain) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = cap_score(v[e], A.cap) * cs::LOG2E;
-            }
-            if (biased) {
-              if (!A.positions || t0 + c0 + 32 <= old) {
-                const float base = (float)(pq - t0 - c0);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = fmaf(-slope, base - (float)e, v[e]);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const int t = t0 + c0 + e, pk = t < s.len ? key_position(A, s.row0, old, t) : 0;
-                  v[e] = fmaf(-slope, (float)(pq - pk), v[e]);
+                if (t + 32 > old) {
+                  const int j0 = t - old;        // new row of bit 0 (negative: earlier keys)
+                  uint32_t fresh;                // bits of the new rows that the row sees
+                  if (!A.mask) {
+                    const int upto = i - j0;     // bits 0 .. upto
+                    fresh = upto < 0 ? 0u : upto >= 31 ? 0xffffffffu : (2u << upto) - 1u;
+                  } else {
+                    const uint32_t* words = A.mask + (long long)(s.row0 + i) * A.words;
+                    const int wi = j0 >> 5, sh = j0 & 31;
+                    const uint32_t lo = wi >= 0 && wi < A.words ? words[wi] : 0u;
+                    const uint32_t hi = wi + 1 >= 0 && wi + 1 < A.words ? words[wi + 1] : 0u;
+                    fresh = __funnelshift_r(lo, hi, sh);
+                  }
+                  const uint32_t new_bits = j0 >= 0 ? 0xffffffffu : j0 <= -32 ? 0u : 0xffffffffu << -j0;
+                  seen &= ~new_bits | fresh;
+                  if (A.window && A.positions)
+                    for (int e = max(0, -j0); e < 32 && j0 + e < s.n; ++e)
+                      if (pq - A.positions[s.row0 + j0 + e] >= A.window) seen &= ~(1u << e);
                 }
               }
-            }
-            if (hidden) {
+              const bool by_place = !A.positions || t + 32 <= old;
+              const float base = (float)(pq - t);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (seen >> e) & 1u ? v[e] : -INFINITY;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, v[e]);
+              for (int e = 0; e < 32; ++e) {
+                float y = __uint_as_float(v[e]) * mult;
+                if (!plain) y = cap_score(y, A.cap) * cs::LOG2E;
+                if (biased) {
+                  float far = base - (float)e;
+                  if (!by_place && t + e < s.len) far = (float)(pq - key_position(A, s.row0, old, t + e));
+                  y = fmaf(-slope, far, y);
+                }
+                if (!((seen >> e) & 1u)) y = -INFINITY;
+                mx = fmaxf(mx, y);
+                v[e] = __float_as_uint(y);
+              }
+            };
+            special_scores(a, t0, dead0);
+            special_scores(b, t0 + 32, dead1);
             __syncwarp();
-            tmem_st32(ts + c0, v);
           }
-          tmem_wait_st();
-        }
-        const float mul = special ? 1.f : mult;
-        // ---- the reference maximum moves only when it lags: then O and l are rescaled ----
-        const bool grow = mx > m_ref + cs::LAG;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float to_m = fmaxf(mx, m_ref), f = m_ref == -INFINITY ? 0.f : cs::ex2(m_ref - to_m);
-          m_ref = to_m;
-          l2.x *= f;
-          l2.y *= f;
-          if (k > 0) {
-            wait_warp(o_done(x), (mine - 1) & 1);
-            umma::fence_after_sync();
+          const float mul = special ? 1.f : mult;
+          // ---- the reference maximum moves only when it lags: then O and l are rescaled ----
+          // (The products of the half before are over by now; waiting for them every time keeps this
+          // thread at most one phase behind the barrier, whose parity would mislead it otherwise.)
+          if (outs > 0) wait_warp(o_done(x), (outs - 1) & 1);
+          const bool grow = mx > m_ref + cs::LAG;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float to_m = fmaxf(mx, m_ref), f = m_ref == -INFINITY ? 0.f : cs::ex2(m_ref - to_m);
+            m_ref = to_m;
+            l2.x *= f;
+            l2.y *= f;
+            if (k + hf > 0) {
+              umma::fence_after_sync();
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              float v[32];
-              umma::tmem_ld32(to + c0, v);
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                float v[16];
+                tmem_ld16(to + c0, v);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] *= f;
-              tmem_st32(to + c0, v);
+                for (int e = 0; e < 16; ++e) v[e] *= f;
+                tmem_st16(to + c0, v);
+              }
             }
-            tmem_wait_st();
           }
-        }
-        const float ref = m_ref == -INFINITY ? 0.f : cs::SHIFT - m_ref;
-        const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(ref, ref);
-#pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 64) {
-          uint32_t a[32], b[32], h[32];
-          tmem_ld32_async(ts + c0, a);
-          tmem_ld32_async(ts + c0 + 32, b);
-          tmem_wait_ld(a, b);
+          const float ref = m_ref == -INFINITY ? 0.f : cs::SHIFT - m_ref;
+          const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(ref, ref);
+          uint32_t h[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const uint32_t* v = e < 16 ? a + 2 * e : b + 2 * (e - 16);
@@ -755,28 +871,16 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
             l2 = __fadd2_rn(l2, p);
             h[e] = ca::h2u(__floats2half2_rn(p.x, p.y));
           }
-          tmem_st32u(ts + c0 / 2, h);
+          tmem_st32u(tsh, h);
+          tmem_wait_st();
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) arrive(p_full(x, hf));
+          ++outs;
         }
-        tmem_wait_st();
-        umma::fence_before_sync();
-        bar_sync(1 + x, 128);
-        const uint32_t use = seen_of[i_buf]++;
-        if (issuer) {
-          umma::fence_after_sync();
-          if (wait(v_full(i_buf), use & 1)) {
-            umma::fence_after_sync();
-            const uint32_t vt = sma + S::V + i_buf * S::OPND;
-#pragma unroll
-            for (int kk = 0; kk < TILE / 16; ++kk)
-              mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, umma::smem_desc(vt + kk * 2048, BOX, 1024), id_o,
-                     (k | kk) != 0);
-            umma::mma_commit(o_done(x));
-            umma::mma_commit(v_free(i_buf));
-          }
-          if (k + 1 < tiles) issue_scores(PAIR ? i_buf ^ 1 : i_buf);
-        }
+        ++seen_of[i_buf];
       }
-      if (tiles > 0) wait_warp(o_done(x), (mine - 1) & 1);
+      if (tiles > 0) wait_warp(o_done(x), (outs - 1) & 1);
       const bool whole = jobs.u0 == 0 && jobs.u1 == jobs.units;
       const float l = l2.x + l2.y;
       const uint32_t o0 = tmem + 256 + lanes, o1 = o0 + 128;
@@ -836,18 +940,13 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
         A.notes[blockIdx.x] = make_int4(
             jobs.b, jobs.h, jobs.rt, cs::pieces_until(total, parts, blockIdx.x, jobs.base + jobs.units));
       }
-      // O is read and Q no longer needed before the next job's first product
+      // O is read (and, where the groups share it, Q no longer needed) before the next job's products
       umma::fence_before_sync();
-      if constexpr (PAIR) bar_sync(1 + x, 128);
-      else bar_sync(3, 256);
+      if constexpr (!PAIR) bar_sync(3, 256);
       umma::fence_after_sync();
     }
-    if (issuer) {
-      umma::mma_commit(drain(x));
-      if (!ct::mbar_wait(drain(x), 0)) *abort_flag = 1;
-      if (*abort_flag) raise_status(A.a.status, DEV_ERR_TIMEOUT);
-    }
   }
+  __syncwarp();
   umma::fence_before_sync();
   __syncthreads();
   if (warp == 0) {

@@ -275,6 +275,33 @@ def test_attend_long_and_ragged():
             assert ((got[p.starts[b]:p.starts[b + 1]] - want).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("n,G,heads", [(16, 4, 1), (40, 1, 2), (33, 4, 1), (70, 8, 1)])
+@pytest.mark.parametrize("lens", [[70000], [9000, 40000, 130, 33000]])
+def test_attend_many_tiles_in_one_block(n, G, heads, lens):
+    """Rows by the dozen over enough keys that every thread block has many tiles of a job, and parts
+    of several jobs; the keys repeat, so the answer is that of one repetition."""
+    D, page, rep = 64, 64, 128
+    p = Paged([rep], [1], heads, D, page, (4, 4))
+    reps = [x // rep for x in lens]
+    table = torch.zeros(len(lens), max(reps) * 2 + 2, dtype=torch.int32, device="cuda")
+    for b, r in enumerate(reps):
+        table[b, :2 * r] = p.batch.page_table[0].repeat(r)[:2 * r]
+    starts = torch.arange(0, n * len(lens) + 1, n, dtype=torch.int32, device="cuda")
+    batch = J.CacheBatch(table, torch.tensor([r * rep for r in reps], dtype=torch.int32, device="cuda"), starts, n)
+    mask = torch.full((n * len(lens), -(-n // 32)), -1, dtype=torch.int32, device="cuda")    # all new rows seen
+    q = torch.randn(n * len(lens), heads * G, D).half()
+    got = p.cache.attend(0, q.cuda(), batch, mask=mask)
+    p.cache.check()
+    k, v = (torch.from_numpy(p.values[kv][0]) for kv in range(2))
+    s = torch.einsum("nhgd,lhd->nhgl", q.double().view(-1, heads, G, D), k) / D ** 0.5
+    w = s.softmax(-1)
+    want = torch.einsum("nhgl,lhd->nhgd", w, v).reshape(q.shape)
+    mag = torch.einsum("nhgl,lhd->nhgd", w, v.abs()).reshape(q.shape)
+    d = float(2.0 ** -11 * torch.einsum("nhgd,lhd->nhgl", q.double().view(-1, heads, G, D).abs(), k.abs()).max() / D ** 0.5)
+    tol = mag * (2 * np.expm1(2 * d) + 2.0 ** -10 + 2.0 ** -17) + 2.0 ** -11 * want.abs() + 1e-6
+    assert ((got.double().cpu() - want).abs() <= tol).all()
+
+
 def test_strided_queries_and_outputs():
     p = Paged([30, 50], [2, 2], 2, 64, 16, (4, 4))
     x = torch.randn(4, 8, 64, device="cuda").bfloat16()

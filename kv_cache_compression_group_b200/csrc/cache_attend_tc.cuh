@@ -12,12 +12,13 @@
 //   * two softmax warpgroups with score and output accumulators of their own (all 512 columns of
 //     tensor memory).  With 256 rows each has 128 of them and both use every tile, which halves the
 //     dequantisation; with 128 rows one takes the even and the other the odd tiles, joined at the
-//     end.  A thread has one row and takes 64 keys at a time: scores to registers, maximum, weights,
-//     and these as fp16 over the scores.  The reference maximum may lag by 2^8, so rescaling O, a
-//     pass through tensor memory, is rare after the first tiles;
-//   * one warp issues the products.  A group's scores lie in two halves of 64 keys: while its warps
-//     are at the one, O += P V (P from tensor memory) and the next tile's S = Q K^T of the other run.
-//     (With whole tiles, a group waited for its own products: 4600 cycles per tile instead.)
+//     end.  A thread has one row: it reads its scores twice (maximum, then weights) and writes the
+//     weights as fp16 over the scores.  The reference maximum may lag by 2^8, so rescaling O, a pass
+//     through tensor memory, is rare after the first tiles;
+//   * one thread issues the products, O += P V (P from tensor memory) and then the group's next
+//     S = Q K^T, of the one group while the other is at its softmax.  (Scores in two halves of 64
+//     keys, to overlap a group's products with its own softmax, were slower: a product with N = 64
+//     waits for the shared memory that Q is read from again, and there are twice the commits.)
 // What bounds it at D = 128: the two products take 1024 cycles per 128 x 128 tile, its 16384
 // exponentials 1024 at 16 per cycle, and the instructions of softmax (about 450 per scheduler) and
 // of dequantisation (about 600, once per 256 rows) come next to them.
@@ -86,21 +87,29 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-// umma::mbar_wait with a hint that lets the thread sleep for longer between its looks
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = umma::global_ns();
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (umma::global_ns() - t0 > umma::kWaitNs) return false;
+// A bounded wait for a phase of a barrier that looks before anything else: reading the clock, as
+// umma::mbar_wait does, or the flag takes longer than most waits.  A look lets the thread sleep for up
+// to 20 us, so the bound is between some milliseconds and about three seconds; who gives up raises
+// the flag, which ends the other waits too.
+constexpr int LOOKS = 1 << 17;
+__device__ __forceinline__ bool mbar_look(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  for (int i = 0; i < LOOKS; ++i) {
+    if (mbar_look(bar, parity)) return true;
+    if (*abort_flag) return false;
   }
+  *abort_flag = 1;
+  return false;
 }
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -398,7 +407,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   constexpr int ROWS = PAIR ? 256 : 128;
   extern __shared__ unsigned char ct_raw[];
   unsigned char* sm = (unsigned char*)(((uintptr_t)ct_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t bars[21 + 2 * RING];
+  __shared__ __align__(8) uint64_t bars[17 + 2 * RING];
   __shared__ uint32_t tmem_slot;
   __shared__ int aborted, s_b;
   __shared__ long long s_sum[THREADS / 32], s_base;
@@ -407,29 +416,24 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
   __shared__ float s_max[2][2][128];                      // largest |q| of [group][half of the features][row]
   __shared__ float2 s_ml[2][128];                         // maximum and sum of [group][row]
   volatile int* abort_flag = &aborted;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp's number by a shuffle: so the compiler knows that it, and the roles' branches, are uniform
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t sma = umma::smem_u32(sm), bar0 = umma::smem_u32(bars);
   // barriers of buffer i: K written, K no longer needed, V written, V no longer needed; of group x:
-  // Q laid out; of its half h: S = Q K^T done, P written, O += P V done; all products done; of the ring
+  // S = Q K^T done, P written, Q laid out, the job's last O += P V done; all products done; of the ring
   auto k_full = [&](int i) { return bar0 + 8 * i; };
   auto k_free = [&](int i) { return bar0 + 16 + 8 * i; };
   auto v_full = [&](int i) { return bar0 + 32 + 8 * i; };
   auto v_free = [&](int i) { return bar0 + 48 + 8 * i; };
-  auto s_done = [&](int x, int h) { return bar0 + 64 + 16 * x + 8 * h; };
-  auto p_full = [&](int x, int h) { return bar0 + 96 + 16 * x + 8 * h; };
-  auto q_full = [&](int x) { return bar0 + 128 + 8 * x; };
-  auto o_done = [&](int x) { return bar0 + 144 + 8 * x; };   // (of one half, then of the other)
-  auto ring_full = [&](int i) { return bar0 + 160 + 8 * i; };
-  auto ring_free = [&](int i) { return bar0 + 160 + 8 * (RING + i); };
-  const uint32_t drained = bar0 + 160 + 16 * RING;
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (*abort_flag) return false;
-    if (ct::mbar_wait(bar, parity)) return true;
-    *abort_flag = 1;
-    return false;
-  };
+  auto s_done = [&](int x) { return bar0 + 64 + 8 * x; };
+  auto p_full = [&](int x) { return bar0 + 80 + 8 * x; };
+  auto q_full = [&](int x) { return bar0 + 96 + 8 * x; };
+  auto o_done = [&](int x) { return bar0 + 112 + 8 * x; };
+  auto ring_full = [&](int i) { return bar0 + 128 + 8 * i; };
+  auto ring_free = [&](int i) { return bar0 + 128 + 8 * (RING + i); };
+  const uint32_t drained = bar0 + 128 + 16 * RING;
   auto wait_warp = [&](uint32_t bar, uint32_t parity) {   // by whole warps
-    wait(bar, parity);
+    ct::mbar_wait(bar, parity, abort_flag);
     __syncwarp();
   };
 
@@ -439,12 +443,10 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
       umma::mbar_init(k_free(i), 1);
       umma::mbar_init(v_full(i), 8);
       umma::mbar_init(v_free(i), 1);
-      for (int h = 0; h < 2; ++h) {
-        umma::mbar_init(s_done(i, h), 1);
-        umma::mbar_init(p_full(i, h), 4);
-      }
-      umma::mbar_init(q_full(i), PAIR ? 4 : 8);
+      umma::mbar_init(s_done(i), 1);
+      umma::mbar_init(p_full(i), 4);
       umma::mbar_init(o_done(i), 1);
+      umma::mbar_init(q_full(i), PAIR ? 4 : 8);
     }
     for (int i = 0; i < RING; ++i) {
       umma::mbar_init(ring_full(i), 1);
@@ -536,67 +538,70 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
           publish(row, (tile - jobs.u0) & 1, live);
         }
       publish(-1, 0, 0);
-    } else if (warp == 16) {
+    } else if (warp == 16 && lane == 0) {
       // ================= the products =================
-      constexpr uint32_t id_s = idesc(64, false), id_o = idesc(D, true);
+      // (One thread, and a wait only where a phase is new: what this thread spends between two
+      // products is time in which none may run.)
+      constexpr uint32_t id_s = idesc(128, false), id_o = idesc(D, true);
       const uint64_t kd = umma::smem_desc(sma + S::K, 16, 1024), vd = umma::smem_desc(sma + S::V, BOX, 1024);
-      uint32_t k_uses[2] = {0u, 0u}, v_uses[2] = {0u, 0u}, done[2] = {0u, 0u}, round = 0;
-      auto going = [&]() { return !__any_sync(0xffffffffu, *abort_flag); };
-      // S = Q K^T of group x, half hf of the keys of buffer i; `last`: nobody else needs K after it
-      auto scores_of = [&](int x, int hf, int i, bool last) {
-        wait_warp(k_full(i), k_uses[i] & 1);
+      uint32_t k_par = 0u, v_par = 0u, p_par = 0u, q_par = 0u;   // bit i: parity of the next phase of barrier i
+      bool go = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) { go = ct::mbar_wait(bar, parity, abort_flag) && go; };
+      // S = Q K^T of group x with the K of buffer i; first / last: of those who need this K
+      auto scores_of = [&](int x, int i, bool first, bool last) {
+        if (first) {
+          wait(k_full(i), (k_par >> i) & 1);
+          k_par ^= 1u << i;
+        }
         umma::fence_after_sync();
         const uint64_t qd = umma::smem_desc(sma + (PAIR && x ? S::Q2 : S::Q), 16, 1024);
-        const uint64_t kh = kd + (uint64_t)((i * S::OPND + hf * 64 * 128) >> 4);
-        if (going() && elect_one()) {
+        const uint64_t kh = kd + (uint64_t)((i * S::OPND) >> 4);
+        if (!go) return;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = (uint64_t)(((k / 4) * BOX + (k % 4) * 32) >> 4);
-            mma_ss(tmem + 128 * x + 64 * hf, qd + off, kh + off, id_s, k != 0);
-          }
-          umma::mma_commit(s_done(x, hf));
-          if (last) umma::mma_commit(k_free(i));
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = (uint64_t)(((k / 4) * BOX + (k % 4) * 32) >> 4);
+          mma_ss(tmem + 128 * x, qd + off, kh + off, id_s, k != 0);
         }
-        __syncwarp();
-        if (last) ++k_uses[i];
+        umma::mma_commit(s_done(x));
+        if (last) umma::mma_commit(k_free(i));
       };
-      for (; jobs.w < jobs.w1; jobs.next(A), ++round) {
+      for (; jobs.w < jobs.w1; jobs.next(A)) {
         const int count = jobs.u1 - jobs.u0;
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-          wait_warp(q_full(PAIR ? x : 0), round & 1);
-          if (PAIR || x < count)
-            for (int hf = 0; hf < 2; ++hf) scores_of(x, hf, PAIR ? 0 : x, hf == 1 && (!PAIR || x == 1));
-        }
-        for (int k = 0; k < (PAIR ? count : (count + 1) / 2); ++k) {
-          for (int hf = 0; hf < 2; ++hf) {
-            for (int x = 0; x < 2; ++x) {
-              const int jt = PAIR ? k : 2 * k + x, i = jt & 1;
-              if (jt >= count) break;
-              wait_warp(p_full(x, hf), done[x] & 1);
-              wait_warp(v_full(i), v_uses[i] & 1);
-              umma::fence_after_sync();
-              const bool last = hf == 1 && (!PAIR || x == 1);
-              if (going() && elect_one()) {
-                const uint64_t vh = vd + (uint64_t)((i * S::OPND + hf * 64 * 128) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 64 * hf + 8 * kk, vh + (uint64_t)((kk * 2048) >> 4),
-                         id_o, (k | hf | kk) != 0);
-                umma::mma_commit(o_done(x));
-                if (last) umma::mma_commit(v_free(i));
-              }
-              __syncwarp();
-              if (last) ++v_uses[i];
-              if (hf == 1) ++done[x];
-              if (jt + (PAIR ? 1 : 2) < count) scores_of(x, hf, PAIR ? i ^ 1 : i, last);
-            }
+          if (PAIR || x == 0) {
+            wait(q_full(x), (q_par >> x) & 1);
+            q_par ^= 1u << x;
           }
+          if (PAIR || x < count) scores_of(x, PAIR ? 0 : x, !PAIR || x == 0, !PAIR || x == 1);
+        }
+#pragma unroll 1
+        for (int e = 0; e < (PAIR ? 2 * count : count); ++e) {
+          // tile jt, group x: in turn
+          const int x = e & 1, jt = PAIR ? e >> 1 : e, i = jt & 1;
+          const bool first = !PAIR || x == 0, last = !PAIR || x == 1, more = jt + (PAIR ? 1 : 2) < count;
+          wait(p_full(x), (p_par >> x) & 1);
+          p_par ^= 1u << x;
+          if (first) {
+            wait(v_full(i), (v_par >> i) & 1);
+            v_par ^= 1u << i;
+          }
+          umma::fence_after_sync();
+          if (go) {
+            const uint64_t vh = vd + (uint64_t)((i * S::OPND) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < TILE / 16; ++kk)
+              mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * kk, vh + (uint64_t)((kk * 2048) >> 4), id_o,
+                     (PAIR ? jt : jt >> 1) != 0 || kk != 0);
+            if (!more) umma::mma_commit(o_done(x));
+            if (last) umma::mma_commit(v_free(i));
+          }
+          if (more) scores_of(x, PAIR ? i ^ 1 : i, first, last);
         }
       }
-      if (elect_one()) umma::mma_commit(drained);
-      __syncwarp();
-      if (!ct::mbar_wait(drained, 0)) *abort_flag = 1;
-      if (*abort_flag && lane == 0) raise_status(A.a.status, DEV_ERR_TIMEOUT);
+      umma::mma_commit(drained);
+      if (!umma::mbar_wait(drained, 0)) *abort_flag = 1;
+      if (*abort_flag) raise_status(A.a.status, DEV_ERR_TIMEOUT);
     }
   } else if (warp >= 8) {
     // ================= dequantising warps =================
@@ -614,12 +619,13 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
       int live, buf;      // tokens that exist, buffers
     };
     RawRegs rk, rv;
-    uint32_t k_uses[2] = {0u, 0u}, v_uses[2] = {0u, 0u}, round = 0;
+    uint32_t used = 0u, k_par = 0u, v_par = 0u, round = 0;   // bit i: buffer i is in use (+ 2: its V); parities
     int slot = 0;
     auto take = [&]() {                        // the next tile of the walk
-      wait_warp(ring_full(slot), round & 1);
+      const bool go = __all_sync(0xffffffffu, ct::mbar_wait(ring_full(slot), round & 1, abort_flag));
       const longlong2 e = s_ring[slot][grp];
-      const Tile t{__any_sync(0xffffffffu, *abort_flag) ? -1 : e.x, (int)e.y, (int)(e.y >> 32)};
+      const Tile t{go ? e.x : -1, (int)e.y, (int)(e.y >> 32)};
+      __syncwarp();
       if (lane == 0) arrive(ring_free(slot));
       if (++slot == RING) {
         slot = 0;
@@ -631,22 +637,24 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
     auto load_v = [&](const Tile& t) { raw_load<VB, D>(rv, vc, vs, t.row, lane, t.live); };
     auto store_k = [&](const Tile& t) {
       const int i = t.buf;
-      if (k_uses[i]) wait_warp(k_free(i), (k_uses[i] - 1) & 1);
+      if ((used >> i) & 1u) wait_warp(k_free(i), (k_par >> i & 1u) ^ 1u);
       raw_store<KB, D>(rk, sma + S::K + i * S::OPND, 16 * grp, lane, magic);
-      if (lane == 0) s_dead[i][k_uses[i] & 1][grp] = (uint16_t)(0xffffu << t.live);
+      if (lane == 0) s_dead[i][k_par >> i & 1u][grp] = (uint16_t)(0xffffu << t.live);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive(k_full(i));
-      ++k_uses[i];
+      used |= 1u << i;
+      k_par ^= 1u << i;
     };
     auto store_v = [&](const Tile& t) {
       const int i = t.buf;
-      if (v_uses[i]) wait_warp(v_free(i), (v_uses[i] - 1) & 1);
+      if ((used >> i) & 4u) wait_warp(v_free(i), (v_par >> i & 1u) ^ 1u);
       raw_store<VB, D>(rv, sma + S::V + i * S::OPND, 16 * grp, lane, magic);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) arrive(v_full(i));
-      ++v_uses[i];
+      used |= 4u << i;
+      v_par ^= 1u << i;
     };
     const Tile none{-1, 0, 0};
     Tile e0 = take(), e1 = none, e2 = none;
@@ -683,9 +691,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
     const uint32_t ts = tmem + 128 * x + lanes, to = tmem + 256 + 128 * x + lanes;
     const uint32_t qt = sma + (PAIR && x ? S::Q2 : S::Q);
     const bool plain = A.cap == 0.f, biased = A.slopes != nullptr;
-    uint32_t mine = 0;                         // tiles of this group so far
-    uint32_t seen_of[2] = {0u, 0u};            // uses of the buffers so far
-    uint32_t outs = 0;                         // products O += P V so far
+    uint32_t s_par = 0u, o_par = 0u, dead_par = 0u;   // parities: of the barriers, and (bit i) of buffer i's use
     for (; jobs.w < jobs.w1; jobs.next(A)) {
       const Seq<ROWS>& s = jobs.s;
       const int old = s.len - s.n, R = s.n * A.G, count = jobs.u1 - jobs.u0;
@@ -760,109 +766,118 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
       float m_ref = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       const int tiles = PAIR ? count : (count - x + 1) / 2;     // of this group in this part
-      for (int k = 0; k < tiles; ++k, ++mine) {
+      for (int k = 0; k < tiles; ++k) {
         const int jt = PAIR ? k : 2 * k + x, i_buf = jt & 1;
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          const int t0 = s.first + (jobs.u0 + jt) * TILE + 64 * hf;
-          const uint32_t tsh = ts + 64 * hf;
-          wait_warp(s_done(x, hf), mine & 1);    // S is there, and s_dead, written before the K tile was
-          umma::fence_after_sync();
-          const volatile uint32_t* dd =
-              reinterpret_cast<const volatile uint32_t*>(s_dead[i_buf][seen_of[i_buf] & 1]) + 2 * hf;
-          const uint32_t dead0 = dd[0], dead1 = dd[1];
-          const bool hidden = (dead0 | dead1) != 0u || t0 + 64 > sure || t0 < edge;
-          const bool special = hidden || biased || !plain;
-          uint32_t a[32], b[32];
-          tmem_ld32_async(tsh, a);
-          tmem_ld32_async(tsh + 32, b);
-          tmem_wait_ld(a, b);
-          float mx = -INFINITY;
-          if (!special) {
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const int t0 = s.first + (jobs.u0 + jt) * TILE;
+        // S is there, s_dead (written before the K tile was), and the O += P V of the tile before, which
+        // this S was queued behind, is over
+        wait_warp(s_done(x), s_par);
+        s_par ^= 1u;
+        umma::fence_after_sync();
+        const volatile uint32_t* dd = reinterpret_cast<const volatile uint32_t*>(s_dead[i_buf][dead_par >> i_buf & 1u]);
+        dead_par ^= 1u << i_buf;
+        const bool hidden = (dd[0] | dd[1] | dd[2] | dd[3]) != 0u || t0 + TILE > sure || t0 < edge;
+        const bool special = hidden || biased || !plain;
+        float mx = -INFINITY;
+        if (!special) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c0 = 0; c0 < 128; c0 += 64) {
+            uint32_t a[32], b[32];
+            tmem_ld32_async(ts + c0, a);
+            tmem_ld32_async(ts + c0 + 32, b);
+            tmem_wait_ld(a, b);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               m4[e & 3] = fmaxf(m4[e & 3], fmaxf(__uint_as_float(a[e]), __uint_as_float(b[e])));
-            mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * mult;
-          } else {
-            // capped, biased and masked scores in base 2
-            auto special_scores = [&](uint32_t (&v)[32], int t, uint32_t dead) {   // v[e]: key t + e
-              uint32_t seen = 0xffffffffu;
-              if (hidden) {
-                seen = ~dead;
-                if (A.window) {
-                  // keys in the sequence at positions above pq - window; new rows below
-                  const int lowest = max(pq, old) - A.window + 1 - t;
-                  const int low = A.positions ? min(lowest, max(old - t, 0)) : lowest;
-                  if (low >= 32) seen = 0u;
-                  else if (low > 0) seen &= 0xffffffffu << low;
-                }
-                if (t + 32 > old) {
-                  const int j0 = t - old;        // new row of bit 0 (negative: earlier keys)
-                  uint32_t fresh;                // bits of the new rows that the row sees
-                  if (!A.mask) {
-                    const int upto = i - j0;     // bits 0 .. upto
-                    fresh = upto < 0 ? 0u : upto >= 31 ? 0xffffffffu : (2u << upto) - 1u;
-                  } else {
-                    const uint32_t* words = A.mask + (long long)(s.row0 + i) * A.words;
-                    const int wi = j0 >> 5, sh = j0 & 31;
-                    const uint32_t lo = wi >= 0 && wi < A.words ? words[wi] : 0u;
-                    const uint32_t hi = wi + 1 >= 0 && wi + 1 < A.words ? words[wi + 1] : 0u;
-                    fresh = __funnelshift_r(lo, hi, sh);
-                  }
-                  const uint32_t new_bits = j0 >= 0 ? 0xffffffffu : j0 <= -32 ? 0u : 0xffffffffu << -j0;
-                  seen &= ~new_bits | fresh;
-                  if (A.window && A.positions)
-                    for (int e = max(0, -j0); e < 32 && j0 + e < s.n; ++e)
-                      if (pq - A.positions[s.row0 + j0 + e] >= A.window) seen &= ~(1u << e);
-                }
-              }
-              const bool by_place = !A.positions || t + 32 <= old;
-              const float base = (float)(pq - t);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                float y = __uint_as_float(v[e]) * mult;
-                if (!plain) y = cap_score(y, A.cap) * cs::LOG2E;
-                if (biased) {
-                  float far = base - (float)e;
-                  if (!by_place && t + e < s.len) far = (float)(pq - key_position(A, s.row0, old, t + e));
-                  y = fmaf(-slope, far, y);
-                }
-                if (!((seen >> e) & 1u)) y = -INFINITY;
-                mx = fmaxf(mx, y);
-                v[e] = __float_as_uint(y);
-              }
-            };
-            special_scores(a, t0, dead0);
-            special_scores(b, t0 + 32, dead1);
-            __syncwarp();
           }
-          const float mul = special ? 1.f : mult;
-          // ---- the reference maximum moves only when it lags: then O and l are rescaled ----
-          // (The products of the half before are over by now; waiting for them every time keeps this
-          // thread at most one phase behind the barrier, whose parity would mislead it otherwise.)
-          if (outs > 0) wait_warp(o_done(x), (outs - 1) & 1);
-          const bool grow = mx > m_ref + cs::LAG;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float to_m = fmaxf(mx, m_ref), f = m_ref == -INFINITY ? 0.f : cs::ex2(m_ref - to_m);
-            m_ref = to_m;
-            l2.x *= f;
-            l2.y *= f;
-            if (k + hf > 0) {
-              umma::fence_after_sync();
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * mult;
+        } else {
+          // capped, biased and masked scores in base 2, written back
 #pragma unroll 1
-              for (int c0 = 0; c0 < D; c0 += 16) {
-                float v[16];
-                tmem_ld16(to + c0, v);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] *= f;
-                tmem_st16(to + c0, v);
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            float v[32];
+            __syncwarp();
+            umma::tmem_ld32(ts + c0, v);
+            const int t = t0 + c0;             // v[e]: key t + e
+            uint32_t seen = 0xffffffffu;
+            if (hidden) {
+              seen = ~dd[c0 / 32];
+              if (A.window) {
+                // keys in the sequence at positions above pq - window; new rows below
+                const int lowest = max(pq, old) - A.window + 1 - t;
+                const int low = A.positions ? min(lowest, max(old - t, 0)) : lowest;
+                if (low >= 32) seen = 0u;
+                else if (low > 0) seen &= 0xffffffffu << low;
+              }
+              if (t + 32 > old) {
+                const int j0 = t - old;        // new row of bit 0 (negative: earlier keys)
+                uint32_t fresh;                // bits of the new rows that the row sees
+                if (!A.mask) {
+                  const int upto = i - j0;     // bits 0 .. upto
+                  fresh = upto < 0 ? 0u : upto >= 31 ? 0xffffffffu : (2u << upto) - 1u;
+                } else {
+                  const uint32_t* words = A.mask + (long long)(s.row0 + i) * A.words;
+                  const int wi = j0 >> 5, sh = j0 & 31;
+                  const uint32_t lo = wi >= 0 && wi < A.words ? words[wi] : 0u;
+                  const uint32_t hi = wi + 1 >= 0 && wi + 1 < A.words ? words[wi + 1] : 0u;
+                  fresh = __funnelshift_r(lo, hi, sh);
+                }
+                const uint32_t new_bits = j0 >= 0 ? 0xffffffffu : 0xffffffffu << -j0;
+                seen &= ~new_bits | fresh;
+                if (A.window && A.positions)
+                  for (int e = max(0, -j0); e < 32 && j0 + e < s.n; ++e)
+                    if (pq - A.positions[s.row0 + j0 + e] >= A.window) seen &= ~(1u << e);
               }
             }
+            const bool by_place = !A.positions || t + 32 <= old;
+            const float base = (float)(pq - t);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float y = v[e] * mult;
+              if (!plain) y = cap_score(y, A.cap) * cs::LOG2E;
+              if (biased) {
+                float far = base - (float)e;
+                if (!by_place && t + e < s.len) far = (float)(pq - key_position(A, s.row0, old, t + e));
+                y = fmaf(-slope, far, y);
+              }
+              if (!((seen >> e) & 1u)) y = -INFINITY;
+              mx = fmaxf(mx, y);
+              v[e] = y;
+            }
+            __syncwarp();
+            tmem_st16(ts + c0, *reinterpret_cast<const float(*)[16]>(v));
+            tmem_st16(ts + c0 + 16, *reinterpret_cast<const float(*)[16]>(v + 16));
           }
-          const float ref = m_ref == -INFINITY ? 0.f : cs::SHIFT - m_ref;
-          const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(ref, ref);
-          uint32_t h[32];
+          tmem_wait_st();
+        }
+        const float mul = special ? 1.f : mult;
+        // ---- the reference maximum moves only when it lags: then O and l are rescaled ----
+        const bool grow = mx > m_ref + cs::LAG;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float to_m = fmaxf(mx, m_ref), f = m_ref == -INFINITY ? 0.f : cs::ex2(m_ref - to_m);
+          m_ref = to_m;
+          l2.x *= f;
+          l2.y *= f;
+          if (k > 0) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              float v[16];
+              tmem_ld16(to + c0, v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] *= f;
+              tmem_st16(to + c0, v);
+            }
+          }
+        }
+        const float ref = m_ref == -INFINITY ? 0.f : cs::SHIFT - m_ref;
+        const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(ref, ref);
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 64) {
+          uint32_t a[32], b[32], h[32];
+          tmem_ld32_async(ts + c0, a);
+          tmem_ld32_async(ts + c0 + 32, b);
+          tmem_wait_ld(a, b);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const uint32_t* v = e < 16 ? a + 2 * e : b + 2 * (e - 16);
@@ -871,16 +886,17 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
             l2 = __fadd2_rn(l2, p);
             h[e] = ca::h2u(__floats2half2_rn(p.x, p.y));
           }
-          tmem_st32u(tsh, h);
-          tmem_wait_st();
-          umma::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) arrive(p_full(x, hf));
-          ++outs;
+          tmem_st32u(ts + c0 / 2, h);
         }
-        ++seen_of[i_buf];
+        tmem_wait_st();
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(p_full(x));
       }
-      if (tiles > 0) wait_warp(o_done(x), (outs - 1) & 1);
+      if (tiles > 0) {
+        wait_warp(o_done(x), o_par);
+        o_par ^= 1u;
+      }
       const bool whole = jobs.u0 == 0 && jobs.u1 == jobs.units;
       const float l = l2.x + l2.y;
       const uint32_t o0 = tmem + 256 + lanes, o1 = o0 + 128;

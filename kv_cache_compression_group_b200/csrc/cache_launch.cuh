@@ -63,7 +63,7 @@ jolt_status launch_many(const CacheAttendArgs& A, cudaStream_t st) {
   constexpr int smem = ct::Smem<D>::bytes(PAIR), rows = PAIR ? 256 : 128;
   CUDA_TRY(cudaFuncSetAttribute(cache_many_rows_kernel<D, KB, VB, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   CUDA_TRY(launch_after(cache_many_rows_kernel<D, KB, VB, PAIR>, dim3(MANY_BLOCKS), ct::THREADS, smem, A, st));
-  CUDA_TRY(launch_after(cache_join_kernel<D, rows, 8, 1>, dim3(MANY_BLOCKS, rows / 8), 256, 0, A, st));
+  CUDA_TRY(launch_after(cache_join_rows_kernel<D, rows>, dim3(MANY_BLOCKS, rows / 8), 256, 0, A, st));
   return JOLT_OK;
 }
 

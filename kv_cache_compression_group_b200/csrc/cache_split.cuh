@@ -113,10 +113,45 @@ __device__ __forceinline__ void store_out(const CacheAttendArgs& A, int D, int r
   else reinterpret_cast<bf16*>(A.out)[at] = __float2bfloat16_rn(y);
 }
 
-// Join the pieces of the job that begins in block blockIdx.x, one CTA per PER rows of its tile: the
-// pieces' maxima and sums first, then the weighted sums in the pieces' order, GROUPS threads per feature
-// taking every GROUPS-th piece (a few rows of few jobs have up to 74 pieces each; 128 rows of many
-// jobs mostly two).
+// Join the pieces of the job that begins in block blockIdx.x.  Both kernels add a row's pieces in
+// their order.
+
+// Many rows, mostly of two or three pieces: a warp per row, no exchange between them.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) cache_join_rows_kernel(CacheAttendArgs A) {
+  constexpr int REC = D + 4, V = D / 32;
+  cs::wait_for_predecessor();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int4 note = A.notes[c0];
+  const int b = note.x, h = note.y, tile = note.z, count = note.w;
+  if (tile < 0) return;
+  const int row0 = A.a.starts[b], R = (A.a.starts[b + 1] - row0) * A.G;
+  const int mine = blockIdx.y * 8 + (threadIdx.x >> 5), row = tile * ROWS + mine;
+  if (row >= R) return;
+  const float* p = A.pieces + ((2ll * c0 + 1) * ROWS + mine) * REC;
+  float o[V], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < count; ++k) {
+    const float2 ml = *reinterpret_cast<const float2*>(p + D);
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = p[32 * i + lane];
+    const float top = fmaxf(m, ml.x);
+    const float f = l == 0.f ? 0.f : cs::ex2(m - top), g = ml.y == 0.f ? 0.f : cs::ex2(ml.x - top);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = fmaf(g, v[i], f * o[i]);
+    l = fmaf(g, ml.y, f * l);
+    m = top;
+    p += (k == 0 ? 1 : 2) * (long long)ROWS * REC;   // the next block's slot 0
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) store_out(A, D, row0 + row / A.G, h * A.G + row % A.G, 32 * i + lane, o[i], l, m);
+}
+
+// Few rows of few jobs, which may have up to 74 pieces each: one CTA per PER rows, the pieces' maxima
+// and sums first, then the weighted sums, GROUPS threads per feature taking every GROUPS-th piece.
 template <int D, int ROWS, int PER, int GROUPS>
 __global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendArgs A) {
   constexpr int REC = D + 4, MOST = 592, AT_ONCE = 256 / (D * GROUPS);

@@ -447,47 +447,67 @@ class QuantCache:
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = pools
         self.n_layers, self.n_heads, self.head_dim = n_layers, n_heads, head_dim
         self.n_pages, self.page_size, self.bits = n_pages, page_size, bits
-        self.device = pools[0].device
+        self.device = pools[0].device        # with its index
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._layers = []
         for layer in range(n_layers):
             self._layers.append(CCache(n_heads, head_dim, page_size, n_pages, bits[0], bits[1],
                                        *(t[layer].data_ptr() for t in pools)))
         # the shape is checked now rather than at the first call
-        nbytes = ctypes.c_size_t()
-        with torch.cuda.device(self.device):
-            _check(lib().jolt_cache_attend_scratch_size(ctypes.byref(self._layers[0]), ctypes.byref(CCacheBatch()),
-                                                        n_heads, ctypes.byref(nbytes)))
+        self._status_ptr = self.status.data_ptr()
+        self._scratch_bytes(self._layers[0], CCacheBatch(), n_heads)
 
-    def _call(self, layer, batch, rows, tensors, stream):
-        """The layer's pool, the batch for this many rows, and the stream of a call."""
+    def _scratch_bytes(self, c, b, nq):
+        nbytes = ctypes.c_size_t()
+        _check(lib().jolt_cache_attend_scratch_size(c, b, nq, ctypes.byref(nbytes)))
+        return nbytes.value
+
+    def _run(self, call, stream, *args):
+        """call(*args, stream) on the cache's device: on the given stream, else on the current one."""
+        idx = self.device.index
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(idx)
+        elif hasattr(stream, "cuda_stream"):
+            stream = stream.cuda_stream
+        if torch.cuda.current_device() == idx:
+            status = call(*args, stream)
+        else:
+            with torch.cuda.device(idx):
+                status = call(*args, stream)
+        if status:
+            _check(status)
+
+    def _call(self, layer, batch, rows, *tensors):
+        """The layer's pool, and the batch for this many rows."""
         if not 0 <= layer < self.n_layers:
             raise ValueError(f"layer {layer} not in [0, {self.n_layers})")
+        device = self.device
         for t in (batch, *tensors):
-            if t is not None and t.device != self.device:
-                raise ValueError(f"everything must be on the cache's device {self.device}")
+            if t is not None and t.device != device:
+                raise ValueError(f"everything must be on the cache's device {device}")
         b = CCacheBatch.from_buffer_copy(batch._c)
-        b.n_rows, b.status = rows, self.status.data_ptr()
-        return self._layers[layer], b, torch.cuda.current_stream(self.device) if stream is None else stream
+        b.n_rows, b.status = rows, self._status_ptr
+        return self._layers[layer], b
 
     def _rows(self, t, name, heads):
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.head_dim:
+        """Check rows [rows, heads, head_dim]; their strides (rows, heads)."""
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self.head_dim:
             raise ValueError(f"{name} must be [rows, {heads}, {self.head_dim}]")
-        if t.shape[0] and t.stride(2) != 1:
+        row, head, feature = t.stride()
+        if feature != 1 and shape[0]:
             raise ValueError(f"the features of {name} must be contiguous")
-        return t
+        return row, head
 
     def write(self, layer: int, k: torch.Tensor, v: torch.Tensor, batch: CacheBatch, stream=None):
         """Quantise rows k, v [rows, n_heads, head_dim] (bf16, fp16 or fp32, strided rows and heads)
         into their pages: they become the last rows of the batch's sequences."""
-        self._rows(k, "k", self.n_heads)
-        self._rows(v, "v", self.n_heads)
+        ks = self._rows(k, "k", self.n_heads)
+        vs = self._rows(v, "v", self.n_heads)
         if k.dtype != v.dtype or k.shape != v.shape or k.dtype not in _CACHE_DTYPES:
             raise ValueError("k and v must have one shape and one of the types bf16, fp16, fp32")
-        c, b, st = self._call(layer, batch, k.shape[0], (k, v), stream)
-        with torch.cuda.device(self.device):
-            _check(lib().jolt_cache_write(c, b, k.data_ptr(), v.data_ptr(), _CACHE_DTYPES[k.dtype], k.stride(0),
-                                          k.stride(1), v.stride(0), v.stride(1), _stream(st)))
+        c, b = self._call(layer, batch, k.shape[0], k, v)
+        self._run(lib().jolt_cache_write, stream, c, b, k.data_ptr(), v.data_ptr(), _CACHE_DTYPES[k.dtype], *ks, *vs)
 
     def read(self, layer: int, batch: CacheBatch, rows: int, dtype=torch.bfloat16, out=None, stream=None):
         """The batch's rows as dense (k, v), each [rows, n_heads, head_dim] of dtype; out: tensors to
@@ -498,14 +518,12 @@ class QuantCache:
             shape = (int(rows), self.n_heads, self.head_dim)
             out = tuple(torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
         k, v = out
-        self._rows(k, "out[0]", self.n_heads)
-        self._rows(v, "out[1]", self.n_heads)
+        ks = self._rows(k, "out[0]", self.n_heads)
+        vs = self._rows(v, "out[1]", self.n_heads)
         if k.dtype != dtype or v.dtype != dtype or k.shape != v.shape or k.shape[0] != rows:
             raise ValueError("out must be two tensors of dtype and rows")
-        c, b, st = self._call(layer, batch, k.shape[0], (k, v), stream)
-        with torch.cuda.device(self.device):
-            _check(lib().jolt_cache_read(c, b, _CACHE_DTYPES[dtype], k.data_ptr(), v.data_ptr(), k.stride(0),
-                                         k.stride(1), v.stride(0), v.stride(1), _stream(st)))
+        c, b = self._call(layer, batch, k.shape[0], k, v)
+        self._run(lib().jolt_cache_read, stream, c, b, _CACHE_DTYPES[dtype], k.data_ptr(), v.data_ptr(), *ks, *vs)
         return k, v
 
     def attend(self, layer: int, q: torch.Tensor, batch: CacheBatch, scale: float = 0.0, softcap: float = 0.0,
@@ -523,49 +541,53 @@ class QuantCache:
         if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % self.n_heads:
             raise ValueError(f"q must be [rows, a multiple of {self.n_heads} heads, {self.head_dim}]")
         rows, nq = q.shape[0], q.shape[1]
-        self._rows(q, "q", nq)
+        qs = self._rows(q, "q", nq)
         if q.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("q must be bf16 or fp16")
+        c, b = self._call(layer, batch, rows, q, out)
+        o = CAttendOptions(scale, softcap, window)
+        if slopes is not None or positions is not None or mask is not None or prefix is not None:
+            self._extras(o, rows, nq, slopes, positions, mask, prefix)
+        if out is None:
+            out = torch.empty((rows, nq, self.head_dim), dtype=q.dtype, device=self.device)
+        elif out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must have q's shape and type")
+        # a scratch of its own for every call: two calls, or two captured graphs, never share one
+        nbytes = self._scratch_bytes(c, b, nq)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self._run(lib().jolt_cache_attend, stream, c, b, o, q.data_ptr(), _CACHE_DTYPES[q.dtype], nq, *qs,
+                  out.data_ptr(), *self._rows(out, "out", nq), scratch.data_ptr(), nbytes)
+        if isinstance(stream, torch.cuda.Stream):
+            scratch.record_stream(stream)
+        return out
+
+    def _extras(self, o, rows, nq, slopes, positions, mask, prefix):
+        """Check the optional tensors of attend and put them into its options."""
         p_out, p_lse = prefix if prefix is not None else (None, None)
         for name, t, shape, dt in (("slopes", slopes, (nq,), torch.float32),
                                    ("positions", positions, (rows,), torch.int32),
                                    ("mask", mask, None, torch.int32),
-                                   ("prefix[0]", p_out, (rows, nq, self.head_dim), torch.float32),
-                                   ("prefix[1]", p_lse, (rows, nq), torch.float32)):
+                                   ("prefix_out", p_out, (rows, nq, self.head_dim), torch.float32),
+                                   ("prefix_lse", p_lse, (rows, nq), torch.float32)):
             if t is None:
                 continue
             if t.dtype != dt or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
                 raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape or '[rows, words]'}")
-        if mask is not None and (mask.dim() != 2 or mask.shape[0] != rows):
-            raise ValueError("mask must be [rows, words]")
-        c, b, st = self._call(layer, batch, rows, (q, slopes, positions, mask, p_out, p_lse, out), stream)
-        with torch.cuda.device(self.device):
-            if out is None:
-                out = torch.empty((rows, nq, self.head_dim), dtype=q.dtype, device=self.device)
-            elif out.shape != q.shape or out.dtype != q.dtype:
-                raise ValueError("out must have q's shape and type")
-            self._rows(out, "out", nq)
-            nbytes = ctypes.c_size_t()
-            _check(lib().jolt_cache_attend_scratch_size(c, b, nq, ctypes.byref(nbytes)))
-            # a scratch of its own for every call: two calls, or two captured graphs, never share one
-            scratch = torch.empty(nbytes.value, dtype=torch.uint8, device=self.device)
-            o = CAttendOptions(scale, softcap, window, 0 if mask is None else mask.shape[1],
-                               *(None if t is None else t.data_ptr() for t in (slopes, positions, mask, p_out, p_lse)))
-            _check(lib().jolt_cache_attend(c, b, o, q.data_ptr(), _CACHE_DTYPES[q.dtype], nq, q.stride(0),
-                                           q.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
-                                           scratch.data_ptr(), nbytes.value, _stream(st)))
-            if stream is not None and isinstance(stream, torch.cuda.Stream):
-                scratch.record_stream(stream)
-        return out
+            if t.device != self.device:
+                raise ValueError(f"everything must be on the cache's device {self.device}")
+            setattr(o, name, t.data_ptr())
+        if mask is not None:
+            if mask.dim() != 2 or mask.shape[0] != rows:
+                raise ValueError("mask must be [rows, words]")
+            o.mask_words = mask.shape[1]
 
     def check(self, stream=None):
         """Raise what the kernels of this cache's calls found so far (synchronises), and clear it."""
-        with torch.cuda.device(self.device):
-            st = torch.cuda.current_stream(self.device) if stream is None else stream
-            status = lib().jolt_cache_check(self.status.data_ptr(), _stream(st))
-            if status:
-                self.status.zero_()
-            _check(status)
+        try:
+            self._run(lib().jolt_cache_check, stream, self._status_ptr)
+        except JoltError:
+            self.status.zero_()
+            raise
 
 
 def read_header(blob: torch.Tensor, stream=None):

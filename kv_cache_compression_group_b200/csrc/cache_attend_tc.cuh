@@ -81,6 +81,10 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+// 16 rows of a page, contiguous; address and size are multiples of 16 bytes
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -533,6 +537,14 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
               row = row_index(A.c, page, jobs.h, t);
               live = min(16, jobs.s.len - t);
             }
+          }
+          if (lane < 8 && live > 0) {
+            // the rows into L2, as far ahead as the ring: the loads to registers are one tile ahead, which
+            // covers L2's latency but not that of DRAM
+            prefetch_l2(A.c.codes[0] + row * (D * KB / 8), 2 * D * KB);
+            prefetch_l2(A.c.scales[0] + row * (D / 16), 4 * D);
+            prefetch_l2(A.c.codes[1] + row * (D * VB / 8), 2 * D * VB);
+            prefetch_l2(A.c.scales[1] + row * (D / 16), 4 * D);
           }
           __syncwarp();
           publish(row, (tile - jobs.u0) & 1, live);

@@ -14,7 +14,7 @@ SOURCES = ["jolt_api.cu", "cache_api.cu", "cache_few_d64.cu", "cache_few_d128.cu
            "cache_many_d64.cu", "cache_many_d128.cu"]
 DEPS = ["jolt_api.cu", "common.cuh", "gemm.cuh", "kernels.cuh", "misc.cuh", "umma.cuh", "eig_cluster.cuh", "chol.cuh",
         "fp16_exact.cuh", "table_tc.cuh", "attend.cuh", "eig_large.cuh", "host.cuh", "cache_api.cu", "cache.cuh", "cache_split.cuh",
-        "cache_attend.cuh", "cache_attend_tc.cuh", "cache_launch.cuh",
+        "cache_attend.cuh", "cache_attend_codes.cuh", "cache_attend_tc.cuh", "cache_launch.cuh",
         "cache_few_d64.cu", "cache_few_d128.cu", "cache_many_d64.cu", "cache_many_d128.cu"]
 CACHE = [d for d in DEPS if d.startswith("cache") and d.endswith(".cuh")]
 

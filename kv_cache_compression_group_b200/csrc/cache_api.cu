@@ -105,7 +105,8 @@ struct Scratch {
 Scratch attend_scratch(const CacheArgs& c, const BatchArgs& a, int nq) {
   const long long rows = (long long)a.max_new * (nq / c.H);
   const int nt = few_tiles(rows);
-  const size_t blocks = rows > FEW_ROWS ? MANY_BLOCKS : few_blocks(c, nt), tile = rows > 128 ? 256 : rows > FEW_ROWS ? 128 : 8 * nt;
+  // (the codes' kernel has at most four blocks per SM, of at most 16 rows)
+  const size_t blocks = rows > FEW_ROWS ? MANY_BLOCKS : rows <= 16 ? 148 * 4 : few_blocks(c, nt), tile = rows > 128 ? 256 : rows > FEW_ROWS ? 128 : rows <= 16 ? 16 : 8 * nt;
   Scratch s;
   Bump m;
   s.notes = m.take(sizeof(int4) * blocks);
@@ -117,7 +118,7 @@ Scratch attend_scratch(const CacheArgs& c, const BatchArgs& a, int nq) {
 template <int D>
 jolt_status launch_cache_attend(const CacheAttendArgs& A, cudaStream_t st) {
   const long long rows = (long long)A.a.max_new * A.G;
-  if (rows <= FEW_ROWS) return launch_few_rows<D>(A, few_tiles(rows), st);
+  if (rows <= FEW_ROWS) return launch_few_rows<D>(A, st);
   return launch_many_rows<D>(A, rows > 128, st);
 }
 

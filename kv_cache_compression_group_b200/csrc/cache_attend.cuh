@@ -255,6 +255,96 @@ __device__ __forceinline__ int cache_units(const CacheAttendArgs& A, int b, int 
   return (len - first + unit - 1) / unit;
 }
 
+// The units of a block: all sequences' units are summed, and the sequence in which the block's range
+// begins is looked for (by one warp, 32 sequences at a time).  false: the block has none.
+struct BlockRange {
+  long long total, w0, w1, base;   // units in all; this block's; first unit of sequence b
+  int parts, b;                    // blocks that have units
+};
+__device__ __forceinline__ bool block_units(const CacheAttendArgs& A, BlockRange& r) {
+  using namespace ca;
+  __shared__ long long s_sum[WARPS], s_base;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int row0, n, len, first;
+  long long total = 0;
+  for (int b = tid; b < A.a.B; b += WARPS * 32)
+    total += (long long)cache_units(A, b, UNIT, row0, n, len, first) * A.c.H;
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
+  if (lane == 0) s_sum[warp] = total;
+  __syncthreads();
+  r.total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+  r.parts = (int)min((long long)gridDim.x, r.total);
+  if ((int)blockIdx.x >= r.parts) return false;
+  r.w0 = cs::range_start(r.total, r.parts, blockIdx.x);
+  r.w1 = cs::range_start(r.total, r.parts, blockIdx.x + 1);
+  if (warp == 0) {
+    long long base = 0;
+    for (int b0 = 0; b0 < A.a.B; b0 += 32) {
+      const int b = b0 + lane;
+      long long u = b < A.a.B ? (long long)cache_units(A, b, UNIT, row0, n, len, first) * A.c.H : 0, sum = u;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, sum, k);
+        if (lane >= k) sum += up;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, base + sum > r.w0);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          s_b = b;
+          s_base = base + sum - u;
+        }
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  __syncthreads();
+  r.b = s_b;
+  r.base = s_base;
+  return true;
+}
+
+// The four warps' sums of a job's rows joined, and stored or left as a piece.  merge: [warp][row][D + 4];
+// the outputs are `factor` times what it holds.
+template <int D, int ROWS>
+__device__ __forceinline__ void merge_warps(const CacheAttendArgs& A, const float* merge, int b, int h, int row0, int R,
+                                            int u0, int u1, int units, float factor, const BlockRange& range,
+                                            long long base) {
+  using namespace ca;
+  const int tid = threadIdx.x;
+  const bool whole = u0 == 0 && u1 == units;
+  for (int idx = tid; idx < ROWS * D; idx += WARPS * 32) {
+    const int r = idx / D, d = idx % D;
+    if (r >= R) break;
+    float top = -INFINITY, y = 0.f, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) top = fmaxf(top, merge[(k * ROWS + r) * (D + 4) + D]);
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      const float* rec = merge + (k * ROWS + r) * (D + 4);
+      const float f = rec[D + 1] == 0.f ? 0.f : cs::ex2(rec[D] - top);
+      y = fmaf(f, factor * rec[d], y);
+      sum = fmaf(f, rec[D + 1], sum);
+    }
+    if (whole) {
+      store_out(A, D, row0 + r / A.G, h * A.G + r % A.G, d, y, sum, top);
+    } else {
+      float* rec = A.pieces + ((2ll * blockIdx.x + (u0 == 0 ? 1 : 0)) * ROWS + r) * (D + 4);
+      rec[d] = y;
+      if (d == 0) {
+        rec[D] = top;
+        rec[D + 1] = sum;
+      }
+    }
+  }
+  if (!whole && u0 == 0 && tid == 0) {
+    const long long end = base + (long long)(h + 1) * units;
+    A.notes[blockIdx.x] = make_int4(b, h, 0, cs::pieces_until(range.total, range.parts, blockIdx.x, end));
+  }
+}
+
 // What a warp needs of its job; the arrays are the kernel's registers.
 template <int NT>
 struct FewJob {
@@ -422,53 +512,17 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
   RowInfo* rows = reinterpret_cast<RowInfo*>(ca_smem + S::QF);          // [8 NT]
   unsigned char* ring = ca_smem + S::FIXED;
   float* merge = reinterpret_cast<float*>(ring);                        // [warp][row][D + 4], after the ring
-  __shared__ long long s_sum[WARPS], s_base;
-  __shared__ int s_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   constexpr int bk = KB, bv = VB;
   unsigned char* mine = ring + warp * stages(D, bk, bv) * stage_bytes(D, bk, bv);
-  int row0, n, len, first;
-
   cs::wait_for_predecessor();
   cs::let_successor_start();
-  // ---- this block's range of units: all units, then the sequence in which the range begins ----
-  long long total = 0;
-  for (int b = tid; b < A.a.B; b += WARPS * 32)
-    total += (long long)cache_units(A, b, UNIT, row0, n, len, first) * A.c.H;
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
-  if (lane == 0) s_sum[warp] = total;
+  BlockRange range;
   if (tid == 0) A.notes[blockIdx.x] = make_int4(0, 0, -1, 0);
-  __syncthreads();
-  total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-  const int parts = (int)min((long long)gridDim.x, total);
-  if ((int)blockIdx.x >= parts) return;
-  long long w = cs::range_start(total, parts, blockIdx.x);
-  const long long w1 = cs::range_start(total, parts, blockIdx.x + 1);
-  if (warp == 0) {
-    long long base = 0;
-    for (int b0 = 0; b0 < A.a.B; b0 += 32) {
-      const int b = b0 + lane;
-      long long u = b < A.a.B ? (long long)cache_units(A, b, UNIT, row0, n, len, first) * A.c.H : 0, sum = u;
-#pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, sum, k);
-        if (lane >= k) sum += up;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, base + sum > w);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          s_b = b;
-          s_base = base + sum - u;
-        }
-        break;
-      }
-      base += __shfl_sync(0xffffffffu, sum, 31);
-    }
-  }
-  __syncthreads();
-  int b = s_b;
-  long long base = s_base;
+  if (!block_units(A, range)) return;
+  const long long w1 = range.w1;
+  long long w = range.w0, base = range.base;
+  int b = range.b, row0, n, len, first;
   const bool plain = A.cap == 0.f;
 
   while (w < w1 && b < A.a.B) {
@@ -597,35 +651,7 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
         }
       }
     __syncthreads();
-    const bool whole = u0 == 0 && u1 == units;
-    for (int idx = tid; idx < 8 * NT * D; idx += WARPS * 32) {
-      const int r = idx / D, d = idx % D;
-      if (r >= R) break;
-      float top = -INFINITY, y = 0.f, sum = 0.f;
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) top = fmaxf(top, merge[(k * 8 * NT + r) * (D + 4) + D]);
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        const float* rec = merge + (k * 8 * NT + r) * (D + 4);
-        const float f = rec[D + 1] == 0.f ? 0.f : cs::ex2(rec[D] - top);
-        y = fmaf(f, 2.f * rec[d], y);       // two: the operands are halves
-        sum = fmaf(f, rec[D + 1], sum);
-      }
-      if (whole) {
-        store_out(A, D, row0 + r / A.G, h * A.G + r % A.G, d, y, sum, top);
-      } else {
-        float* rec = A.pieces + ((2ll * blockIdx.x + (u0 == 0 ? 1 : 0)) * 8 * NT + r) * (D + 4);
-        rec[d] = y;
-        if (d == 0) {
-          rec[D] = top;
-          rec[D + 1] = sum;
-        }
-      }
-    }
-    if (!whole && u0 == 0 && tid == 0) {
-      const long long end = base + (long long)(h + 1) * units;
-      A.notes[blockIdx.x] = make_int4(b, h, 0, cs::pieces_until(total, parts, blockIdx.x, end));
-    }
+    merge_warps<D, 8 * NT>(A, merge, b, h, row0, R, u0, u1, units, 2.f, range, base);   // two: the operands are halves
     w += u1 - u0;
   }
 }

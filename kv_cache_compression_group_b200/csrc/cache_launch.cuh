@@ -4,6 +4,7 @@
 #pragma once
 
 #include "cache_attend.cuh"
+#include "cache_attend_codes.cuh"
 #include "cache_attend_tc.cuh"
 #include "host.cuh"
 
@@ -50,6 +51,16 @@ cudaError_t launch_after(K kernel, dim3 grid, int threads, size_t smem, const Ca
 
 
 template <int D, int NT, int KB, int VB>
+jolt_status launch_codes(const CacheAttendArgs& A, cudaStream_t st) {
+  using S = cc::Smem<D, NT, KB, VB>;
+  constexpr int blocks = 148 * cc::blocks_per_sm<D, NT, KB, VB>();
+  CUDA_TRY(cudaFuncSetAttribute(cache_codes_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES));
+  CUDA_TRY(launch_after(cache_codes_kernel<D, NT, KB, VB>, dim3(blocks), ca::WARPS * 32, S::BYTES, A, st));
+  CUDA_TRY(launch_after(cache_join_kernel<D, S::ROWS, 1, 256 / D>, dim3(blocks, A.a.max_new * A.G), 256, 0, A, st));
+  return JOLT_OK;
+}
+
+template <int D, int NT, int KB, int VB>
 jolt_status launch_few(const CacheAttendArgs& A, cudaStream_t st) {
   const int smem = ca::Smem<D, NT>::bytes(KB, VB), blocks = few_blocks(A.c, NT);
   CUDA_TRY(cudaFuncSetAttribute(cache_few_rows_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
@@ -82,24 +93,38 @@ jolt_status launch_many_bits(const CacheAttendArgs& A, cudaStream_t st) {
   }
 }
 
-template <int D, int NT>
-jolt_status launch_few_bits(const CacheAttendArgs& A, cudaStream_t st) {
-  switch (A.c.bits[0] * 16 + A.c.bits[1]) {
-    case 0x22: return launch_few<D, NT, 2, 2>(A, st);
-    case 0x24: return launch_few<D, NT, 2, 4>(A, st);
-    case 0x28: return launch_few<D, NT, 2, 8>(A, st);
-    case 0x42: return launch_few<D, NT, 4, 2>(A, st);
-    case 0x44: return launch_few<D, NT, 4, 4>(A, st);
-    case 0x48: return launch_few<D, NT, 4, 8>(A, st);
-    case 0x82: return launch_few<D, NT, 8, 2>(A, st);
-    case 0x84: return launch_few<D, NT, 8, 4>(A, st);
-    default: return launch_few<D, NT, 8, 8>(A, st);
+// a few rows: the codes' kernel where they fit its n-tiles, else the other
+template <int D, int KB, int VB>
+jolt_status launch_few_rows_of(const CacheAttendArgs& A, cudaStream_t st) {
+  constexpr int R = cc::rows_of(KB, VB);
+  const long long rows = (long long)A.a.max_new * A.G;
+  if (rows <= R) return launch_codes<D, 1, KB, VB>(A, st);
+  if (rows <= 2 * R) return launch_codes<D, 2, KB, VB>(A, st);
+  switch (few_tiles(rows)) {
+    case 1: return launch_few<D, 1, KB, VB>(A, st);
+    case 2: return launch_few<D, 2, KB, VB>(A, st);
+    default: return launch_few<D, 4, KB, VB>(A, st);
   }
 }
 
-// the narrow kernel with nt n-tiles, and its join
 template <int D>
-jolt_status launch_few_rows(const CacheAttendArgs& A, int nt, cudaStream_t st);
+jolt_status launch_few_bits(const CacheAttendArgs& A, cudaStream_t st) {
+  switch (A.c.bits[0] * 16 + A.c.bits[1]) {
+    case 0x22: return launch_few_rows_of<D, 2, 2>(A, st);
+    case 0x24: return launch_few_rows_of<D, 2, 4>(A, st);
+    case 0x28: return launch_few_rows_of<D, 2, 8>(A, st);
+    case 0x42: return launch_few_rows_of<D, 4, 2>(A, st);
+    case 0x44: return launch_few_rows_of<D, 4, 4>(A, st);
+    case 0x48: return launch_few_rows_of<D, 4, 8>(A, st);
+    case 0x82: return launch_few_rows_of<D, 8, 2>(A, st);
+    case 0x84: return launch_few_rows_of<D, 8, 4>(A, st);
+    default: return launch_few_rows_of<D, 8, 8>(A, st);
+  }
+}
+
+// up to FEW_ROWS rows of a KV head, and the join
+template <int D>
+jolt_status launch_few_rows(const CacheAttendArgs& A, cudaStream_t st);
 
 // the tensor-core kernel with jobs of 128 rows or (pair) 256, and its join
 template <int D>

@@ -92,15 +92,26 @@ def tree(rng, news, width):
     return np.array(mask, np.uint32).reshape(-1, words), np.array(depth, np.int32)
 
 
+def magnitude(v):
+    """|v| + (v - lo) of stored values [..., D], numpy or torch; lo, the block's lower end, is its least
+    value, or below it by less than fp16's step there, 2^-10 |lo|, which |v| covers."""
+    blocks = v.reshape(*v.shape[:-1], v.shape[-1] // 16, 16)
+    low = blocks.min(-1, keepdims=True) if isinstance(v, np.ndarray) else blocks.min(-1, keepdim=True).values
+    return (abs(blocks) + (blocks - low)).reshape(v.shape)
+
+
 def plain_attend(p, q, scale=0.0, softcap=0.0, window=0, slopes=None, positions=None, mask=None, prefix=None,
                  skip=(), lost=()):
     """(output, bound) float64 [rows, n_q_heads, D].  q float64.  skip: sequences the call leaves
     out; lost: (sequence, page column) pairs whose keys nobody sees.
 
-    The bound: the stored values and the weights enter the products rounded to fp16 (half a step is
-    2^-11 of the value, and 2^-25 for a value below the normal range), so a score is off by at most
-    d = 2^-11 scale sum |q_d k_d| (+ fp32 sums), every normalised weight by a factor e^(2d), and the
-    output by (e^(2d) - 1) 2 sum p|v| + 2 2^-11 sum p|v| + fp32 sums."""
+    The bound, with u = 2^-11 (half a step of fp16; 2^-25 for a value below its normal range): the
+    stored values enter the products rounded to fp16, so a score is off by at most
+    d = u scale sum |q_d k_d| (+ fp32 sums), every normalised weight by a factor e^(2d), and the
+    output by (e^(2d) - 1) 2 sum p|v|.  Beside that, either the weights and the values are rounded, 2 u
+    sum p|v|; or, where the products take the codes, v = lo + c step is summed as sum fl(p) lo +
+    sum fl(fl(p) step) c: the first rounding of p is common to both and costs u sum p|v|, the second
+    u sum p c step = u sum p (v - lo).  Both are at most 2 u sum p (|v| + v - lo) (see magnitude)."""
     rows, nq, D = q.shape
     G = nq // p.H
     out, tol = np.full(q.shape, np.nan), np.zeros(q.shape)
@@ -131,17 +142,18 @@ def plain_attend(p, q, scale=0.0, softcap=0.0, window=0, slopes=None, positions=
                 if slopes is not None:
                     s = s - float(slopes[h]) * (pq - pos_k[seen])
                 d = scale * (np.abs(k) @ np.abs(x)) * (2.0 ** -11 + 2.0 ** -20) + 2.0 ** -20 * np.abs(s) + scale * 2.0 ** -24 * np.abs(x).sum()
-                vs, d = v, (d.max() if d.size else 0.0)
+                vs, ms, d = v, magnitude(v), (d.max() if d.size else 0.0)
                 if prefix is not None:
                     s = np.append(s, prefix[1][r0 + i, h])
                     vs = np.concatenate((v, prefix[0][r0 + i, h][None]))
+                    ms = np.concatenate((ms, np.abs(prefix[0][r0 + i, h])[None]))
                 if not s.size or s.max() == -np.inf:
                     out[r0 + i, h] = 0.0
                     continue
                 w = np.exp(s - s.max())
                 w /= w.sum()
                 out[r0 + i, h] = w @ vs
-                mag = w @ np.abs(vs) + 2.0 ** -14
+                mag = w @ ms + 2.0 ** -14
                 tol[r0 + i, h] = mag * (2 * math.expm1(2 * d) + 2 * 2.0 ** -11 + 2.0 ** -18)
     return out, tol
 

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import oracle as O
-from cache_helpers import HALF_STEP, Paged, check_attend, plain_attend, quantised, tree
+from cache_helpers import HALF_STEP, Paged, magnitude, check_attend, plain_attend, quantised, tree
 from kv_cache_compression_group_b200 import jolt as J
 from kv_cache_compression_group_b200 import synth
 
@@ -269,7 +269,7 @@ def test_attend_long_and_ragged():
             i, t = torch.arange(n, device="cuda"), torch.arange(lens[b] + n, device="cuda")
             s.masked_fill_((t[None] > lens[b] + i[:, None])[:, None, None], -float("inf"))
             want = torch.einsum("nhgl,lhd->nhgd", s.softmax(-1), v).reshape(n, H * G, D).cpu()
-            mag = torch.einsum("nhgl,lhd->nhgd", s.softmax(-1), v.abs()).reshape(n, H * G, D).cpu()
+            mag = torch.einsum("nhgl,lhd->nhgd", s.softmax(-1), magnitude(v)).reshape(n, H * G, D).cpu()
             d = float(2.0 ** -11 * torch.einsum("nhgd,lhd->nhgl", x.view(n, H, G, D).abs(), k.abs()).max() / D ** 0.5)
             tol = mag * (2 * np.expm1(2 * d) + 2.0 ** -10 + 2.0 ** -17) + 2.0 ** -11 * want.abs() + 1e-6
             assert ((got[p.starts[b]:p.starts[b + 1]] - want).abs() <= tol).all()
@@ -296,7 +296,7 @@ def test_attend_many_tiles_in_one_block(n, G, heads, lens):
     s = torch.einsum("nhgd,lhd->nhgl", q.double().view(-1, heads, G, D), k) / D ** 0.5
     w = s.softmax(-1)
     want = torch.einsum("nhgl,lhd->nhgd", w, v).reshape(q.shape)
-    mag = torch.einsum("nhgl,lhd->nhgd", w, v.abs()).reshape(q.shape)
+    mag = torch.einsum("nhgl,lhd->nhgd", w, magnitude(v)).reshape(q.shape)
     d = float(2.0 ** -11 * torch.einsum("nhgd,lhd->nhgl", q.double().view(-1, heads, G, D).abs(), k.abs()).max() / D ** 0.5)
     tol = mag * (2 * np.expm1(2 * d) + 2.0 ** -10 + 2.0 ** -17) + 2.0 ** -11 * want.abs() + 1e-6
     assert ((got.double().cpu() - want).abs() <= tol).all()
@@ -489,7 +489,7 @@ def test_generation_behind_a_compressed_prompt(n):
                 x = q[i, h].double().cpu()
                 s = (k @ x) / 128 ** 0.5
                 wgt = s.softmax(0)
-                want, mag = wgt @ v, wgt @ v.abs()
+                want, mag = wgt @ v, wgt @ magnitude(v)
                 d = float((k.abs() @ x.abs()).max()) / 128 ** 0.5 * 2.0 ** -11
                 tol = mag * (2 * np.expm1(2 * d) + 2.0 ** -10 + 2e-5) + 2.0 ** -8 * (want.abs() + mag * 0.01) + 1e-6
                 assert ((got[i, h] - want).abs() <= tol).all()

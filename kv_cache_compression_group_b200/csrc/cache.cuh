@@ -11,6 +11,15 @@ namespace pc {
 constexpr int BLK = 16;   // features per (lo, step) pair
 }
 
+namespace cs {
+// Programmatic launch: the kernel before this one in its stream has ended and its writes are seen.
+// (A kernel launched so may start while that one ends; the waiting is all that keeps them apart.)
+__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// the next kernel's blocks may be brought up from here on, to wait for this one's end
+__device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+}  // namespace cs
+
 // one layer's pool; index 0 = K, 1 = V
 struct CacheArgs {
   unsigned char* codes[2];
@@ -276,6 +285,8 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, sizeof(T) == 4 ? 3 : 4) cache_
   const T* src = (kv ? x.x[1] : x.x[0]) + h * (kv ? x.head[1] : x.head[0]) + blk * 16;
   RowCursor at;
   Raw16<16, T> u, next;
+  cs::wait_for_predecessor();
+  cs::let_successor_start();
   if (r0 < r1 && on) load_raw(src + r0 * pitch, vec, next);
   for (int r = r0; r < r1; ++r) {
     u = next;
@@ -319,6 +330,8 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) cache_read_kernel(CacheArgs c,
   const __half2* const scales = kv ? c.scales[1] : c.scales[0];
   T* dst = (kv ? x.x[1] : x.x[0]) + h * (kv ? x.head[1] : x.head[0]) + blk * 16;
   RowCursor at;
+  cs::wait_for_predecessor();
+  cs::let_successor_start();
   for (int r = r0; r < r1; r += READ_AHEAD) {
     // the loads of several rows first
     uint4 q[READ_AHEAD];

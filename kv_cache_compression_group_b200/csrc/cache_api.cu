@@ -82,20 +82,16 @@ dim3 rows_grid(const CacheArgs& c, const BatchArgs& a, RowsArgs<T>* x) {
 template <typename T>
 jolt_status launch_write(const CacheArgs& c, const BatchArgs& a, RowsArgs<const T> x, cudaStream_t st) {
   const dim3 grid = rows_grid(c, a, &x);
-  count_launch();
-  if (c.D == 64) cache_write_kernel<T, 64><<<grid, ROW_WARPS * 32, 0, st>>>(c, a, x);
-  else cache_write_kernel<T, 128><<<grid, ROW_WARPS * 32, 0, st>>>(c, a, x);
-  CUDA_TRY(cudaGetLastError());
+  if (c.D == 64) CUDA_TRY(launch_after(cache_write_kernel<T, 64>, grid, ROW_WARPS * 32, 0, st, c, a, x));
+  else CUDA_TRY(launch_after(cache_write_kernel<T, 128>, grid, ROW_WARPS * 32, 0, st, c, a, x));
   return JOLT_OK;
 }
 
 template <typename T>
 jolt_status launch_read(const CacheArgs& c, const BatchArgs& a, RowsArgs<T> x, cudaStream_t st) {
   const dim3 grid = rows_grid(c, a, &x);
-  count_launch();
-  if (c.D == 64) cache_read_kernel<T, 64><<<grid, ROW_WARPS * 32, 0, st>>>(c, a, x);
-  else cache_read_kernel<T, 128><<<grid, ROW_WARPS * 32, 0, st>>>(c, a, x);
-  CUDA_TRY(cudaGetLastError());
+  if (c.D == 64) CUDA_TRY(launch_after(cache_read_kernel<T, 64>, grid, ROW_WARPS * 32, 0, st, c, a, x));
+  else CUDA_TRY(launch_after(cache_read_kernel<T, 128>, grid, ROW_WARPS * 32, 0, st, c, a, x));
   return JOLT_OK;
 }
 

@@ -261,8 +261,9 @@ struct BlockRange {
   long long total, w0, w1, base;   // units in all; this block's; first unit of sequence b
   int parts, b;                    // blocks that have units
 };
+template <int WARPS>
 __device__ __forceinline__ bool block_units(const CacheAttendArgs& A, BlockRange& r) {
-  using namespace ca;
+  constexpr int UNIT = WARPS * ca::TOK;
   __shared__ long long s_sum[WARPS], s_base;
   __shared__ int s_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -274,7 +275,9 @@ __device__ __forceinline__ bool block_units(const CacheAttendArgs& A, BlockRange
   for (int k = 16; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
   if (lane == 0) s_sum[warp] = total;
   __syncthreads();
-  r.total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+  r.total = 0;
+#pragma unroll
+  for (int k = 0; k < WARPS; ++k) r.total += s_sum[k];
   r.parts = (int)min((long long)gridDim.x, r.total);
   if ((int)blockIdx.x >= r.parts) return false;
   r.w0 = cs::range_start(r.total, r.parts, blockIdx.x);
@@ -306,13 +309,12 @@ __device__ __forceinline__ bool block_units(const CacheAttendArgs& A, BlockRange
   return true;
 }
 
-// The four warps' sums of a job's rows joined, and stored or left as a piece.  merge: [warp][row][D + 4];
+// The warps' sums of a job's rows joined, and stored or left as a piece.  merge: [warp][row][D + 4];
 // the outputs are `factor` times what it holds.
-template <int D, int ROWS>
+template <int D, int ROWS, int WARPS>
 __device__ __forceinline__ void merge_warps(const CacheAttendArgs& A, const float* merge, int b, int h, int row0, int R,
                                             int u0, int u1, int units, float factor, const BlockRange& range,
                                             long long base) {
-  using namespace ca;
   const int tid = threadIdx.x;
   const bool whole = u0 == 0 && u1 == units;
   for (int idx = tid; idx < ROWS * D; idx += WARPS * 32) {
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
   cs::let_successor_start();
   BlockRange range;
   if (tid == 0) A.notes[blockIdx.x] = make_int4(0, 0, -1, 0);
-  if (!block_units(A, range)) return;
+  if (!block_units<WARPS>(A, range)) return;
   const long long w1 = range.w1;
   long long w = range.w0, base = range.base;
   int b = range.b, row0, n, len, first;
@@ -651,7 +653,7 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : NT == 2 ? 3 : 2)
         }
       }
     __syncthreads();
-    merge_warps<D, 8 * NT>(A, merge, b, h, row0, R, u0, u1, units, 2.f, range, base);   // two: the operands are halves
+    merge_warps<D, 8 * NT, WARPS>(A, merge, b, h, row0, R, u0, u1, units, 2.f, range, base);   // two: the operands are halves
     w += u1 - u0;
   }
 }

@@ -62,27 +62,33 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return x;
 }
 
+// warps of a block: eight where two such blocks fit an SM (half as many pieces to join), else four
+template <int NT>
+constexpr int warps_of() { return NT == 1 ? 8 : 4; }
+
 template <int D, int NT, int KB, int VB>
 struct Smem {
+  static constexpr int WARPS = warps_of<NT>();
   static constexpr int ROWS = NT * rows_of(KB, VB);
   static constexpr int QF = (D / 16 + 1) * NT * 32 * 8;       // Q^T fragments, and those of the blocks' sums
-  static constexpr int MERGE = ca::WARPS * ROWS * (D + 4) * 4;
-  static constexpr int RING = ca::WARPS * ca::stages(D, KB, VB) * ca::stage_bytes(D, KB, VB);
+  static constexpr int MERGE = WARPS * ROWS * (D + 4) * 4;
+  static constexpr int RING = WARPS * ca::stages(D, KB, VB) * ca::stage_bytes(D, KB, VB);
   static constexpr int FIXED = (QF + ROWS * 16 + 127) / 128 * 128;
   static constexpr int BYTES = FIXED + (RING > MERGE ? RING : MERGE);
 };
-// blocks of an SM: by registers four or three, by shared memory what 228 KB hold with 1 KB for each
+// blocks of an SM: by registers two of eight warps or three of four, by shared memory what 228 KB hold with 1 KB for each
 template <int D, int NT, int KB, int VB>
 constexpr int blocks_per_sm() {
-  const int by_smem = 228 * 1024 / (Smem<D, NT, KB, VB>::BYTES + 1024), by_regs = NT == 1 ? 4 : 3;
+  const int by_smem = 228 * 1024 / (Smem<D, NT, KB, VB>::BYTES + 1024), by_regs = NT == 1 ? 2 : 3;
   return by_smem < by_regs ? by_smem : by_regs;
 }
 }  // namespace cc
 
 template <int D, int NT, int KB, int VB>
-__global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : 3) cache_codes_kernel(CacheAttendArgs A) {
+__global__ void __launch_bounds__(cc::warps_of<NT>() * 32, NT == 1 ? 2 : 3) cache_codes_kernel(CacheAttendArgs A) {
   using namespace ca;
   using S = cc::Smem<D, NT, KB, VB>;
+  constexpr int WARPS = S::WARPS, UNIT = WARPS * TOK;
   constexpr int RPT = cc::rows_of(KB, VB), ROWS = S::ROWS;
   constexpr int KBPC = 8 / KB, VBPC = 8 / VB;                 // blocks of a chunk
   constexpr int KPER = 32 / KB, CPU = 16 / VB;                // codes of a word of K, of a unit of V
@@ -99,7 +105,7 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : 3) cache_codes_k
   cs::let_successor_start();
   BlockRange range;
   if (tid == 0) A.notes[blockIdx.x] = make_int4(0, 0, -1, 0);
-  if (!block_units(A, range)) return;
+  if (!block_units<WARPS>(A, range)) return;
   const long long w1 = range.w1;
   long long w = range.w0, base = range.base;
   int b = range.b, row0, n, len, first;
@@ -503,7 +509,7 @@ __global__ void __launch_bounds__(ca::WARPS * 32, NT == 1 ? 4 : 3) cache_codes_k
         }
       }
     __syncthreads();
-    merge_warps<D, ROWS>(A, merge, b, h, row0, R, u0, u1, units, 1.f, range, base);
+    merge_warps<D, ROWS, WARPS>(A, merge, b, h, row0, R, u0, u1, units, 1.f, range, base);
     w += u1 - u0;
   }
 }

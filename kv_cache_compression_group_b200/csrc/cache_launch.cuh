@@ -31,32 +31,13 @@ inline int few_blocks(const CacheArgs& c, int nt) {
   return 148 * (by_regs < by_smem ? by_regs : by_smem);
 }
 
-// launch with programmatic stream serialization: the blocks may be brought up while the kernel
-// before them in the stream ends; every thread waits for that end before it reads or writes
-template <typename K>
-cudaError_t launch_after(K kernel, dim3 grid, int threads, size_t smem, const CacheAttendArgs& A, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  count_launch();
-  return cudaLaunchKernelEx(&cfg, kernel, A);
-}
-
-
 template <int D, int NT, int KB, int VB>
 jolt_status launch_codes(const CacheAttendArgs& A, cudaStream_t st) {
   using S = cc::Smem<D, NT, KB, VB>;
   constexpr int blocks = 148 * cc::blocks_per_sm<D, NT, KB, VB>();
   CUDA_TRY(cudaFuncSetAttribute(cache_codes_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES));
-  CUDA_TRY(launch_after(cache_codes_kernel<D, NT, KB, VB>, dim3(blocks), ca::WARPS * 32, S::BYTES, A, st));
-  CUDA_TRY(launch_after(cache_join_kernel<D, S::ROWS, 1, 256 / D>, dim3(blocks, A.a.max_new * A.G), 256, 0, A, st));
+  CUDA_TRY(launch_after(cache_codes_kernel<D, NT, KB, VB>, dim3(blocks), S::WARPS * 32, S::BYTES, st, A));
+  CUDA_TRY(launch_after(cache_join_kernel<D, S::ROWS>, dim3(blocks, (unsigned)ceil_div(A.a.max_new * A.G, 512 / D)), 512, 0, st, A));
   return JOLT_OK;
 }
 
@@ -64,8 +45,8 @@ template <int D, int NT, int KB, int VB>
 jolt_status launch_few(const CacheAttendArgs& A, cudaStream_t st) {
   const int smem = ca::Smem<D, NT>::bytes(KB, VB), blocks = few_blocks(A.c, NT);
   CUDA_TRY(cudaFuncSetAttribute(cache_few_rows_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  CUDA_TRY(launch_after(cache_few_rows_kernel<D, NT, KB, VB>, dim3(blocks), ca::WARPS * 32, smem, A, st));
-  CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT, 1, 256 / D>, dim3(blocks, A.a.max_new * A.G), 256, 0, A, st));
+  CUDA_TRY(launch_after(cache_few_rows_kernel<D, NT, KB, VB>, dim3(blocks), ca::WARPS * 32, smem, st, A));
+  CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT>, dim3(blocks, (unsigned)ceil_div(A.a.max_new * A.G, 512 / D)), 512, 0, st, A));
   return JOLT_OK;
 }
 
@@ -73,8 +54,8 @@ template <int D, int KB, int VB, bool PAIR>
 jolt_status launch_many(const CacheAttendArgs& A, cudaStream_t st) {
   constexpr int smem = ct::Smem<D>::bytes(PAIR), rows = PAIR ? 256 : 128;
   CUDA_TRY(cudaFuncSetAttribute(cache_many_rows_kernel<D, KB, VB, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  CUDA_TRY(launch_after(cache_many_rows_kernel<D, KB, VB, PAIR>, dim3(MANY_BLOCKS), ct::THREADS, smem, A, st));
-  CUDA_TRY(launch_after(cache_join_rows_kernel<D, rows>, dim3(MANY_BLOCKS, rows / 8), 256, 0, A, st));
+  CUDA_TRY(launch_after(cache_many_rows_kernel<D, KB, VB, PAIR>, dim3(MANY_BLOCKS), ct::THREADS, smem, st, A));
+  CUDA_TRY(launch_after(cache_join_rows_kernel<D, rows>, dim3(MANY_BLOCKS, rows / 8), 256, 0, st, A));
   return JOLT_OK;
 }
 

@@ -51,12 +51,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Programmatic launch: the kernel before this one in its stream has ended and its writes are seen.
-// (A kernel launched so may start while that one ends; the waiting is all that keeps them apart.)
-__device__ __forceinline__ void wait_for_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// the next kernel's blocks may be brought up from here on, to wait for this one's end
-__device__ __forceinline__ void let_successor_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // start of block c's range when `total` units are dealt to `parts` blocks
 __device__ __forceinline__ long long range_start(long long total, int parts, int c) { return total * c / parts; }
 // number of blocks from c0 on whose ranges begin before unit `end`
@@ -150,52 +144,36 @@ __global__ void __launch_bounds__(256) cache_join_rows_kernel(CacheAttendArgs A)
   for (int i = 0; i < V; ++i) store_out(A, D, row0 + row / A.G, h * A.G + row % A.G, 32 * i + lane, o[i], l, m);
 }
 
-// Few rows of few jobs, which may have up to 74 pieces each: one CTA per PER rows, the pieces' maxima
-// and sums first, then the weighted sums, GROUPS threads per feature taking every GROUPS-th piece.
-template <int D, int ROWS, int PER, int GROUPS>
-__global__ void __launch_bounds__(256) cache_join_kernel(CacheAttendArgs A) {
-  constexpr int REC = D + 4, MOST = 592, AT_ONCE = 256 / (D * GROUPS);
-  __shared__ float2 ml[AT_ONCE][MOST];      // maximum and sum of every piece
-  __shared__ float part[AT_ONCE][GROUPS][D];
+// Few rows of few jobs, which may have up to 74 pieces each: a CTA takes 512 / D rows, a thread one
+// feature; the pieces' maxima and sums first, then the weighted sums, eight loads under way.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(512) cache_join_kernel(CacheAttendArgs A) {
+  constexpr int REC = D + 4, MOST = 592, PER = 512 / D;
+  __shared__ float2 ml[PER][MOST];      // maximum and sum of every piece
   cs::wait_for_predecessor();
-  const int c0 = blockIdx.x, tid = threadIdx.x;
+  const int c0 = blockIdx.x, slot = threadIdx.x / D, d = threadIdx.x % D;
   const int4 note = A.notes[c0];
   const int b = note.x, h = note.y, tile = note.z, count = note.w;
   if (tile < 0) return;
   const int row0 = A.a.starts[b], R = (A.a.starts[b + 1] - row0) * A.G;
-  const int slot = tid / (D * GROUPS), grp = tid / D % GROUPS, d = tid % D, t = tid % (D * GROUPS);
-  // record of row `mine` in the k-th piece
-  auto rec = [&](int mine, int k) { return A.pieces + ((2ll * (c0 + k) + (k == 0 ? 1 : 0)) * ROWS + mine) * REC; };
-  for (int first = 0; first < PER; first += AT_ONCE) {
-    const int mine = blockIdx.y * PER + first + slot, row = tile * ROWS + mine;
-    float top = -INFINITY, sum = 0.f, y = 0.f;
-    if (row < R)
-      for (int k = t; k < count; k += D * GROUPS) ml[slot][k] = *reinterpret_cast<const float2*>(rec(mine, k) + D);
-    __syncthreads();
-    if (row < R) {
+  const int mine = blockIdx.y * PER + slot, row = tile * ROWS + mine;
+  // record of the row in the k-th piece
+  auto rec = [&](int k) { return A.pieces + ((2ll * (c0 + k) + (k == 0 ? 1 : 0)) * ROWS + mine) * REC; };
+  if (row < R)
+    for (int k = d; k < count; k += D) ml[slot][k] = *reinterpret_cast<const float2*>(rec(k) + D);
+  __syncthreads();
+  if (row >= R) return;
+  float top = -INFINITY, sum = 0.f, y = 0.f;
 #pragma unroll 8
-      for (int k = 0; k < count; ++k) top = fmaxf(top, ml[slot][k].x);
+  for (int k = 0; k < count; ++k) top = fmaxf(top, ml[slot][k].x);
 #pragma unroll 8
-      for (int k = 0; k < count; ++k) {
-        const float2 x = ml[slot][k];
-        const float f = x.y == 0.f ? 0.f : cs::ex2(x.x - top);
-        sum = fmaf(f, x.y, sum);
-      }
-#pragma unroll 8
-      for (int k = grp; k < count; k += GROUPS) {
-        const float2 x = ml[slot][k];
-        y = fmaf(x.y == 0.f ? 0.f : cs::ex2(x.x - top), rec(mine, k)[d], y);
-      }
-      part[slot][grp][d] = y;
-    }
-    __syncthreads();
-    if (row < R && grp == 0) {
-#pragma unroll
-      for (int k = 1; k < GROUPS; ++k) y += part[slot][k][d];
-      store_out(A, D, row0 + row / A.G, h * A.G + row % A.G, d, y, sum, top);
-    }
-    __syncthreads();
+  for (int k = 0; k < count; ++k) {
+    const float2 x = ml[slot][k];
+    const float f = x.y == 0.f ? 0.f : cs::ex2(x.x - top);
+    y = fmaf(f, rec(k)[d], y);
+    sum = fmaf(f, x.y, sum);
   }
+  store_out(A, D, row0 + row / A.G, h * A.G + row % A.G, d, y, sum, top);
 }
 
 }  // namespace jolt

@@ -9,6 +9,7 @@
 #include <string>
 #include <vector>
 
+#include "common.cuh"
 #include "jolt.h"
 
 namespace jolt {
@@ -89,5 +90,23 @@ struct Bump {
     return o;
   }
 };
+
+// Launch with programmatic stream serialization: the blocks may be brought up while the kernel before
+// them in the stream ends; every thread waits for that end before it reads or writes.
+template <typename... P, typename... Q>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const Q&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 
 }  // namespace jolt

@@ -62,13 +62,15 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return x;
 }
 
-// warps of a block: eight where two such blocks fit an SM (half as many pieces to join), else four
-template <int NT>
-constexpr int warps_of() { return NT == 1 ? 8 : 4; }
+// Warps of a block: eight where two such blocks fit an SM, which halves the pieces to join (41 us
+// instead of 45 us for one token over 65536 at 4 bits); but four at 2 bits, where a job is short for
+// its blocks and their common barriers cost more (51 us instead of 54 us for the 40-head case).
+template <int NT, int KB, int VB>
+constexpr int warps_of() { return NT == 1 && KB > 2 && VB > 2 ? 8 : 4; }
 
 template <int D, int NT, int KB, int VB>
 struct Smem {
-  static constexpr int WARPS = warps_of<NT>();
+  static constexpr int WARPS = warps_of<NT, KB, VB>();
   static constexpr int ROWS = NT * rows_of(KB, VB);
   static constexpr int QF = (D / 16 + 1) * NT * 32 * 8;       // Q^T fragments, and those of the blocks' sums
   static constexpr int MERGE = WARPS * ROWS * (D + 4) * 4;
@@ -76,16 +78,17 @@ struct Smem {
   static constexpr int FIXED = (QF + ROWS * 16 + 127) / 128 * 128;
   static constexpr int BYTES = FIXED + (RING > MERGE ? RING : MERGE);
 };
-// blocks of an SM: by registers two of eight warps or three of four, by shared memory what 228 KB hold with 1 KB for each
+// blocks of an SM: by registers 16 warps, or 12 with two n-tiles; by shared memory what 228 KB hold with 1 KB for each
 template <int D, int NT, int KB, int VB>
 constexpr int blocks_per_sm() {
-  const int by_smem = 228 * 1024 / (Smem<D, NT, KB, VB>::BYTES + 1024), by_regs = NT == 1 ? 2 : 3;
+  const int by_smem = 228 * 1024 / (Smem<D, NT, KB, VB>::BYTES + 1024), by_regs = NT == 1 ? 16 / Smem<D, NT, KB, VB>::WARPS : 3;
   return by_smem < by_regs ? by_smem : by_regs;
 }
 }  // namespace cc
 
 template <int D, int NT, int KB, int VB>
-__global__ void __launch_bounds__(cc::warps_of<NT>() * 32, NT == 1 ? 2 : 3) cache_codes_kernel(CacheAttendArgs A) {
+__global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
+                                  NT == 1 ? 16 / cc::warps_of<NT, KB, VB>() : 3) cache_codes_kernel(CacheAttendArgs A) {
   using namespace ca;
   using S = cc::Smem<D, NT, KB, VB>;
   constexpr int WARPS = S::WARPS, UNIT = WARPS * TOK;

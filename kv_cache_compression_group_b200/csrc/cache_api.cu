@@ -100,9 +100,9 @@ struct Scratch {
 };
 Scratch attend_scratch(const CacheArgs& c, const BatchArgs& a, int nq) {
   const long long rows = (long long)a.max_new * (nq / c.H);
-  const int nt = few_tiles(rows);
-  // (the codes' kernel has at most four blocks per SM, of at most 16 rows)
-  const size_t blocks = rows > FEW_ROWS ? MANY_BLOCKS : rows <= 16 ? 148 * 4 : few_blocks(c, nt), tile = rows > 128 ? 256 : rows > FEW_ROWS ? 128 : rows <= 16 ? 16 : 8 * nt;
+  // blocks of the kernel that takes this many rows (or more than it has), and rows of its pieces
+  const size_t blocks = rows > FEW_ROWS ? MANY_BLOCKS : 148 * (rows <= 16 ? 4 : 2);
+  const size_t tile = rows > 128 ? 256 : rows > FEW_ROWS ? 128 : rows <= 16 ? 16 : 32;
   Scratch s;
   Bump m;
   s.notes = m.take(sizeof(int4) * blocks);
@@ -170,6 +170,8 @@ jolt_status jolt_cache_attend_scratch_size(const jolt_cache* cache, const jolt_c
   BatchArgs a;
   JTRY(cache_args(cache, batch, &c, &a));
   if (!bytes || n_q_heads < 1 || n_q_heads % c.H) return fail(JOLT_ERR_INVALID_ARG, "n_q_heads %d", n_q_heads);
+  if ((long long)a.max_new * (n_q_heads / c.H) > (1 << 30))
+    return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "%d new rows of %d query heads", a.max_new, n_q_heads);
   *bytes = attend_scratch(c, a, n_q_heads).total;
   return JOLT_OK;
 }

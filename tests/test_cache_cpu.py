@@ -114,6 +114,10 @@ def test_scratch_size(heads, nq, new):
     assert st == "OK" and 0 < n < 1 << 30
 
 
+def test_more_rows_than_an_index_holds():
+    assert scratch(cache(n_heads=1), batch(max_new=1 << 30, n_rows=1), 8)[0] == "UNSUPPORTED_SHAPE"
+
+
 def test_fp16_is_not_a_type_of_the_compressor():
     o = J.Options((4, 8, 16, 32), (4, 8, 16), (0, 2))
     with pytest.raises(J.JoltError) as e:

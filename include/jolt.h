@@ -337,7 +337,7 @@ jolt_status jolt_cache_read(const jolt_cache* cache, const jolt_cache_batch* bat
 /* What jolt_cache_attend computes beside plain attention. */
 typedef struct {
   float scale;          /* of q . k; 0 = 1 / sqrt(head_dim) */
-  float softcap;        /* c > 0: s = c tanh(s / c), before the bias; 0 = none */
+  float softcap;        /* c > 0: s = c tanh(s / c), before the bias, c in [1e-6, 1e30]; 0 = none */
   int32_t window;       /* w > 0: a row at position p sees keys at positions above p - w only; 0 = all */
   int32_t mask_words;   /* 32-bit words per row of `mask`, at least max_new / 32 */
   const float* slopes_dev;       /* [n_q_heads]: s -= slope * (p_query - p_key); NULL = no bias */
@@ -354,8 +354,9 @@ typedef struct {
  * already written (they are the last n_b of lens[b]).  A row sees the keys before the new rows and
  * those new rows that its mask allows, both inside the window; query head j reads KV head
  * j / (n_q_heads / n_heads).  o = sum_t p_t v_t with p the softmax of s; a row that sees nothing
- * gives its prefix, or zeros.  The stored values enter the products as fp16 (one rounding of
- * lo + code * step), the weights p too; sums, maxima and the softmax are fp32.
+ * gives its prefix, or zeros.  The weights p enter the products as fp16, and with more than a few
+ * rows per KV head the stored values too (one rounding of lo + code * step); sums, maxima and the
+ * softmax are fp32.
  *   q_dev   : [n_rows][n_q_heads][head_dim] of `dtype` (JOLT_BF16 or JOLT_F16), strides in elements
  *   out_dev : the same shape and type, its own strides
  *   scratch_dev: jolt_cache_attend_scratch_size bytes, 256-byte aligned, contents irrelevant; two

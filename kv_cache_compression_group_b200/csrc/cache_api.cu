@@ -189,6 +189,8 @@ jolt_status jolt_cache_attend(const jolt_cache* cache, const jolt_cache_batch* b
   JTRY(jolt_cache_attend_scratch_size(cache, batch, n_q_heads, &need));
   if (!(opts->scale >= 0.f) || !(opts->softcap >= 0.f) || std::isinf(opts->scale) || std::isinf(opts->softcap))
     return fail(JOLT_ERR_INVALID_ARG, "scale %g, softcap %g", opts->scale, opts->softcap);
+  if (opts->softcap > 0.f && (opts->softcap < 1e-6f || opts->softcap > 1e30f))
+    return fail(JOLT_ERR_INVALID_ARG, "softcap %g not in [1e-6, 1e30]", opts->softcap);
   if (opts->window < 0) return fail(JOLT_ERR_INVALID_ARG, "window %d", opts->window);
   if (opts->mask_dev && (opts->mask_words < 1 || opts->mask_words < ceil_div(A.a.max_new, 32)))
     return fail(JOLT_ERR_INVALID_ARG, "mask_words %d for %d new rows", opts->mask_words, A.a.max_new);

@@ -78,10 +78,15 @@ __device__ __forceinline__ bool row_sees(const CacheAttendArgs& A, int row0, int
   return (A.mask[(long long)(row0 + i) * A.words + (j >> 5)] >> (j & 31)) & 1u;
 }
 
-// s = cap tanh(s / cap), with tanh x = 1 - 2 / (e^(2x) + 1)
+// s = cap tanh(s / cap).  tanh x = 1 - 2 / (e^(2x) + 1) is off by some 2^-23, which a large cap makes
+// much of a score; below |x| = 1/4 its series x - x^3/3 + 2x^5/15 - 17x^7/315 is used, whose next term is
+// 62 x^9 / 2835, 2^-21.5 of x there.
 __device__ __forceinline__ float cap_score(float s, float cap) {
-  const float e = cs::ex2(2.f * cs::LOG2E / cap * s);
-  return cap - __fdividef(2.f * cap, e + 1.f);
+  const float x = s * __frcp_rn(cap), x2 = x * x;
+  const float near = fmaf(x2, fmaf(x2, fmaf(x2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f) * s;
+  const float e = cs::ex2(2.f * cs::LOG2E * x);
+  const float far = cap - __fdividef(2.f * cap, e + 1.f);
+  return fabsf(x) < 0.25f ? near : far;
 }
 
 __device__ __forceinline__ float ld_q(const CacheAttendArgs& A, long long at) {

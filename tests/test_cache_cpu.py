@@ -79,7 +79,7 @@ def test_rows_refused():
 
 
 @pytest.mark.parametrize("kw", [dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
-                                dict(softcap=-2.0), dict(softcap=float("nan")), dict(window=-1),
+                                dict(softcap=-2.0), dict(softcap=float("nan")), dict(softcap=1e-9), dict(softcap=1e35), dict(window=-1),
                                 dict(mask=PTR, mask_words=0), dict(prefix_out=PTR), dict(prefix_lse=PTR)])
 def test_options_refused(kw):
     assert attend(cache(), batch(), options(**kw)) == "INVALID_ARG"

@@ -190,7 +190,7 @@ def test_attend_trees(n, D):
 
 
 @pytest.mark.parametrize("n,G", [(1, 4), (2, 8), (3, 8), (12, 8)])
-@pytest.mark.parametrize("opts", [dict(softcap=5.0), dict(scale=0.3), dict(window=1), dict(window=37), dict(window=5000),
+@pytest.mark.parametrize("opts", [dict(softcap=5.0), dict(softcap=1e6), dict(softcap=0.01), dict(scale=0.3), dict(window=1), dict(window=37), dict(window=5000),
                                   dict(slopes=True), dict(softcap=20.0, window=100, slopes=True, scale=0.2),
                                   dict(prefix=True), dict(prefix=True, softcap=8.0, window=64)])
 def test_attend_options(n, G, opts):
@@ -310,6 +310,45 @@ def test_strided_queries_and_outputs():
         out = _strided(torch.zeros_like(x), how)
         got = p.cache.attend(0, _strided(x, how), p.batch, out=out)
         assert got is out and torch.equal(got, want), how
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (3, 8), (9, 8)])
+def test_many_sequences(n, G):
+    """More sequences than threads that look for them, empty ones and ones without new rows among them."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 40, 700).tolist()
+    news = [min(x, int(rng.integers(0, n + 1))) for x in lens]
+    lens[311], news[311] = 900, n
+    p = Paged(lens, news, 1, 64, 16, (4, 4), seed=n, max_new=n)
+    check_attend(p, torch.float16, G)
+    before = [t.clone() for t in p.pools]
+    rows = [p.new_rows(torch.float32, kv).cuda() for kv in range(2)]
+    k, v = p.cache.read(0, p.batch, p.rows, torch.float32)
+    p.cache.write(0, *rows, p.batch)
+    for t, was in zip(p.pools, before):
+        assert torch.equal(t.view(torch.uint8), was.view(torch.uint8))
+    for got, vals in ((k, p.values[0]), (v, p.values[1])):
+        want = np.concatenate([x[len(x) - m:] for x, m in zip(vals, news)])
+        assert np.array_equal(got.cpu().numpy(), want.astype(np.float32))
+    p.cache.check()
+
+
+def test_output_in_place_of_the_queries():
+    p = Paged([5000, 40, 700], [2, 2, 2], 2, 128, 64, (4, 4))
+    q = torch.randn(6, 8, 128, device="cuda").half()
+    want = p.cache.attend(0, q, p.batch)
+    assert torch.equal(p.cache.attend(0, q, p.batch, out=q), want)
+
+
+def test_batch_grows_within_its_bounds():
+    """One batch object whose tensors change between calls: fewer rows than max_new, and more sequences' pages."""
+    p = Paged([100, 60], [8, 1], 2, 64, 16, (8, 8), max_new=40)
+    check_attend(p, torch.bfloat16, 8)                       # max_new * 4 rows choose the wide kernel
+    q = torch.randn(p.rows, 8, 64, device="cuda").bfloat16()
+    wide = p.cache.attend(0, q, p.batch)
+    p.batch = J.CacheBatch(p.batch.page_table, p.batch.lens, p.batch.starts, 8)
+    check_attend(p, torch.bfloat16, 8)
+    assert (wide.float() - p.cache.attend(0, q, p.batch).float()).abs().max() < 0.05
 
 
 # ---- how calls stand next to one another --------------------------------------------------

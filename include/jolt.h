@@ -278,7 +278,8 @@ jolt_status jolt_quant_baseline(const jolt_shape* shape, const void* k_dev, cons
  * the codes: [n_pages][n_heads][page_size][head_dim * bits / 8] bytes, the codes of a row as one
  * little-endian bit string (2 * bits bytes per block); of the scales:
  * [n_pages][n_heads][page_size][head_dim / 16] fp16 pairs (lo, step).  Pointers 16-byte aligned.
- *   head_dim 64 or 128; page_size a power of two in [16, 4096]; bits 2, 4 or 8. */
+ *   head_dim 64 or 128; page_size a power of two in [16, 4096]; bits 2, 4 or 8;
+ *   n_pages * page_size * n_heads below 2^31 (the bytes may pass 2^32). */
 typedef struct {
   int32_t n_heads;
   int32_t head_dim;

@@ -75,9 +75,13 @@ __device__ __forceinline__ int page_at(const BatchArgs& a, const CacheArgs& c, i
   return -1;
 }
 
-// row of head h at position t inside its page: index of its first block
-__device__ __forceinline__ long long row_index(const CacheArgs& c, int page, int h, int t) {
-  return (((long long)page * c.H + h) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
+// row of head h at position t inside its page (a pool has fewer than 2^31 rows; their bytes may pass
+// 32 bits: byte offsets are formed as 32 x 32 -> 64 bit products)
+__device__ __forceinline__ uint32_t row_index(const CacheArgs& c, int page, int h, int t) {
+  return (((uint32_t)page * c.H + h) << c.page_shift) + (t & ((1 << c.page_shift) - 1));
+}
+__device__ __forceinline__ unsigned long long row_bytes(uint32_t row, uint32_t bytes) {
+  return (unsigned long long)row * bytes;
 }
 
 __device__ __forceinline__ float to_f32(bf16 x) { return __bfloat162float(x); }
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32, sizeof(T) == 4 ? 3 : 4) cache_
         mx = fmaxf(mx, v[i]);
       }
     }
-    const long long block = row_index(c, at.page, h, at.t) * LANES + blk;
+    const long long block = (long long)row_index(c, at.page, h, at.t) * LANES + blk;
     unsigned char* codes = pool + block * (2 * bits);
     if (bits == 4) encode_block<4>(v, mn, mx, codes, scales + block);
     else if (bits == 8) encode_block<8>(v, mn, mx, codes, scales + block);
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) cache_read_kernel(CacheArgs c,
       if (!at.ok || !on) continue;
       write |= 1u << k;
       if (at.page < 0) continue;
-      const long long block = row_index(c, at.page, h, at.t) * LANES + blk;
+      const long long block = (long long)row_index(c, at.page, h, at.t) * LANES + blk;
       const unsigned char* src = pool + block * (2 * bits);
       if (bits == 4) *reinterpret_cast<uint2*>(&q[k]) = *reinterpret_cast<const uint2*>(src);
       else if (bits == 8) q[k] = *reinterpret_cast<const uint4*>(src);

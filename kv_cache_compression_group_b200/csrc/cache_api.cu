@@ -21,6 +21,8 @@ jolt_status cache_args(const jolt_cache* c, const jolt_cache_batch* b, CacheArgs
   if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)))
     return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "page_size %d is not a power of two in [16, 4096]", c->page_size);
   if (c->n_pages < 1) return fail(JOLT_ERR_INVALID_ARG, "n_pages %d", c->n_pages);
+  if ((long long)c->n_pages * c->page_size * c->n_heads >= 1LL << 31)
+    return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "a pool of %d pages has 2^31 rows or more", c->n_pages);
   for (int bits : {c->bits_k, c->bits_v})
     if (bits != 2 && bits != 4 && bits != 8)
       return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "cache bits %d not in {2, 4, 8}", bits);
@@ -205,6 +207,7 @@ jolt_status jolt_cache_attend(const jolt_cache* cache, const jolt_cache_batch* b
   A.G = n_q_heads / A.c.H;
   A.scale = opts->scale > 0.f ? opts->scale : (float)(1.0 / sqrt((double)A.c.D));
   A.cap = opts->softcap;
+  A.cap_inv = opts->softcap == 0.f ? 0.f : 1.f / opts->softcap;
   A.window = opts->window;
   A.words = opts->mask_words;
   A.slopes = opts->slopes_dev;

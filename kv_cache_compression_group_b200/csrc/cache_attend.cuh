@@ -388,12 +388,12 @@ __device__ __forceinline__ void few_loop(const CacheAttendArgs& A, const FewJob<
       t_issue += UNIT;
       if (left > 0) page = table[t_issue >> A.c.page_shift];
       if ((unsigned)mine_page < (unsigned)A.c.n_pages) {
-        const long long row = row_index(A.c, mine_page, J.h, t);
+        const uint32_t row = row_index(A.c, mine_page, J.h, t);
         const uint32_t dst = ring + st_issue;
-        copy_rows<KCH>(dst, kdst, kc + row * (D * KB / 8), lane);
-        copy_rows<SCH>(dst, ksd, ks + row * (D / 4), lane);
-        copy_rows<VCH>(dst, vdst, vc + row * (D * VB / 8), lane);
-        copy_rows<SCH>(dst, vsd, vs + row * (D / 4), lane);
+        copy_rows<KCH>(dst, kdst, kc + row_bytes(row, D * KB / 8), lane);
+        copy_rows<SCH>(dst, ksd, ks + row_bytes(row, D / 4), lane);
+        copy_rows<VCH>(dst, vdst, vc + row_bytes(row, D * VB / 8), lane);
+        copy_rows<SCH>(dst, vsd, vs + row_bytes(row, D / 4), lane);
       } else {
         lost |= 1u << ahead;
         raise_status(A.a.status, DEV_ERR_BATCH);
@@ -430,7 +430,7 @@ __device__ __forceinline__ void few_loop(const CacheAttendArgs& A, const FewJob<
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[nt][k] = cap_score(s[nt][k], A.cap) * cs::LOG2E;
+        for (int k = 0; k < 4; ++k) s[nt][k] = cap_score(A, s[nt][k]) * cs::LOG2E;
     }
     if (ragged) {
 #pragma unroll

@@ -124,6 +124,15 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
   const unsigned char* const ks = reinterpret_cast<const unsigned char*>(A.c.scales[0]) + lane * 16;
   const unsigned char* const vs = reinterpret_cast<const unsigned char*>(A.c.scales[1]) + lane * 16;
 
+  // Where this lane reads in a stage (128-byte aligned): word c of chunk q of K's row g is at k_at with q
+  // xored into the chunk's bits, row g + 8 (the same swizzle) a constant further; so are the scales of
+  // block col_grp % KBPC of K's chunks, and the chunks of V's row lane % 16.
+  const uint32_t k_at = swizzled<KCH>(g, 0) + c * 4;
+  const uint32_t ks_at = KBYTES + swizzled<SCH>(g, 0) + (col_grp % KBPC) * 4;
+  const uint32_t lo_at = KBYTES + (D == 128 ? swizzled<2>(g, c >> 1) : g * 16) + (c & 1) * 8;
+  const uint32_t v_at = KBYTES + SBYTES + swizzled<VCH>(lane & 15, VCH == 1 ? 0 : lane >> 4);
+  const uint32_t vs_at = KBYTES + SBYTES + VBYTES + (SCH == 2 ? swizzled<2>(lane & 15, lane >> 4) : (lane & 15) * 16);
+
   while (w < w1 && b < A.a.B) {
     const int units = cache_units(A, b, UNIT, row0, n, len, first);
     if (w >= base + (long long)units * A.c.H) {   // next sequence (those without units are passed over)
@@ -243,12 +252,12 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
         t_issue += UNIT;
         if (left > 0) page = table[t_issue >> A.c.page_shift];
         if ((unsigned)mine_page < (unsigned)A.c.n_pages) {
-          const long long row = row_index(A.c, mine_page, h, t);
+          const uint32_t row = row_index(A.c, mine_page, h, t);
           const uint32_t dst = ring + st_issue;
-          copy_rows<KCH>(dst, kdst, kc + row * (D * KB / 8), lane);
-          copy_rows<SCH>(dst, ksd, ks + row * (D / 4), lane);
-          copy_rows<VCH>(dst, vdst, vc + row * (D * VB / 8), lane);
-          copy_rows<SCH>(dst, vsd, vs + row * (D / 4), lane);
+          copy_rows<KCH>(dst, kdst, kc + row_bytes(row, D * KB / 8), lane);
+          copy_rows<SCH>(dst, ksd, ks + row_bytes(row, D / 4), lane);
+          copy_rows<VCH>(dst, vdst, vc + row_bytes(row, D * VB / 8), lane);
+          copy_rows<SCH>(dst, vsd, vs + row_bytes(row, D / 4), lane);
         } else {
           lost |= 1u << ahead;
           raise_status(A.a.status, DEV_ERR_BATCH);
@@ -271,14 +280,12 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
       if (skip) continue;
       // ---- scores: s[nt][2 t + k] is token g + 8 t, column 2 c + k ----
       float s[NT][4];
-      const uint32_t ksc = sta + KBYTES;
       {
         // lo of blocks 2 c, 2 c + 1 with the blocks' sums
         uint32_t a[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const int row = g + 8 * t;
-          const uint2 x = cc::lds64(ksc + (D == 128 ? swizzled<2>(row, c >> 1) + (c & 1) * 8 : row * 16 + (c & 1) * 8));
+          const uint2 x = cc::lds64(sta + lo_at + 8 * t * SCH * 16);
           a[t] = __byte_perm(x.x, x.y, 0x5410);
         }
 #pragma unroll
@@ -294,10 +301,10 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
         for (int k = 0; k < 4; ++k) acc[nt][k] = 0.f;
 #pragma unroll
       for (int q = 0; q < KCH; ++q) {
-        const uint32_t x0 = cc::lds32(sta + swizzled<KCH>(g, q) + c * 4), x1 = cc::lds32(sta + swizzled<KCH>(g + 8, q) + c * 4);
-        const int blk = q * KBPC + col_grp % KBPC, z = q * KBPC / 4;
-        const float st0 = __high2float(u2h(cc::lds32(ksc + swizzled<SCH>(g, z) + (blk & 3) * 4)));
-        const float st1 = __high2float(u2h(cc::lds32(ksc + swizzled<SCH>(g + 8, z) + (blk & 3) * 4)));
+        const uint32_t at = (sta + k_at) ^ (q * 16u);
+        const uint32_t x0 = cc::lds32(at), x1 = cc::lds32(at + 8 * KCH * 16);
+        const uint32_t sat = ((sta + ks_at) ^ (q * KBPC / 4 * 16u)) + (q * KBPC & 3) * 4;
+        const float st0 = __high2float(u2h(cc::lds32(sat))), st1 = __high2float(u2h(cc::lds32(sat + 8 * SCH * 16)));
         float part[NT][4];
 #pragma unroll
         for (int pp = 0; pp < KPER / 4; ++pp) {
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
             y += __shfl_xor_sync(0xffffffffu, y, 2);
           }
           y *= mult[nt][k & 1];
-          if (!plain) y = cap_score(y, A.cap) * cs::LOG2E;
+          if (!plain) y = cap_score(A, y) * cs::LOG2E;
           s[nt][k] = y;
         }
       if (t0 + TOK > old || t0 < edge) {
@@ -398,15 +405,14 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
         p[nt][1] = transpose8(h2u(__floats2half2_rn(e[2], e[3])));
       }
       // ---- values: (lo, step) of the row's blocks as columns, tokens as pairs ----
-      const uint32_t vcs = sta + KBYTES + SBYTES, vsc = vcs + VBYTES;
       uint32_t sc[2 * SCH];
       if constexpr (SCH == 2) {
         uint32_t x[4];
-        ldsm4t(x, vsc + swizzled<2>(lane & 15, lane >> 4));
+        ldsm4t(x, sta + vs_at);
 #pragma unroll
         for (int k = 0; k < 4; ++k) sc[k] = x[k];
       } else {
-        ldsm2t(sc[0], sc[1], vsc + (lane & 15) * 16);
+        ldsm2t(sc[0], sc[1], sta + vs_at);
       }
       if (t0 + TOK > len) {                // what lies behind the sequence may be anything
         const int t = t0 + 2 * c;
@@ -422,8 +428,8 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
 #pragma unroll
         for (int q2 = 0; q2 < VCH; q2 += 2) {
           uint32_t x[4];
-          if constexpr (VCH == 1) ldsm2t(x[0], x[1], vcs + (lane & 15) * 16);
-          else ldsm4t(x, vcs + swizzled<VCH>(lane & 15, q2 + (lane >> 4)));
+          if constexpr (VCH == 1) ldsm2t(x[0], x[1], sta + v_at);
+          else ldsm4t(x, (sta + v_at) ^ (q2 * 16u));
 #pragma unroll
           for (int u = 0; u < (VCH == 1 ? 1 : 2); ++u) {
             const int q = q2 + u, blk = q * VBPC + b_grp % VBPC, z = q * VBPC / 4, src = 8 * (blk & 3) + 4 + c;

@@ -325,8 +325,8 @@ __device__ __forceinline__ void raw_load_rows(RawRegs& r, const unsigned char* c
 template <int BITS, int D>
 __device__ __forceinline__ void raw_load(RawRegs& r, const unsigned char* codes, const __half2* scales, long long row,
                                          int lane, int live) {
-  codes += row * (D * BITS / 8);
-  scales += row * (D / 16);
+  codes += row_bytes((uint32_t)row, D * BITS / 8);
+  scales += row_bytes((uint32_t)row, D / 16);
   if (live == 16) raw_load_rows<BITS, D, true>(r, codes, scales, lane, live);
   else raw_load_rows<BITS, D, false>(r, codes, scales, lane, live);
 }
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               float y = v[e] * mult;
-              if (!plain) y = cap_score(y, A.cap) * cs::LOG2E;
+              if (!plain) y = cap_score(A, y) * cs::LOG2E;
               if (biased) {
                 float far = base - (float)e;
                 if (!by_place && t + e < s.len) far = (float)(pq - key_position(A, s.row0, old, t + e));

@@ -48,6 +48,7 @@ BAD_CACHES = [(dict(head_dim=96), "UNSUPPORTED_SHAPE"), (dict(head_dim=256), "UN
               (dict(page_size=8), "UNSUPPORTED_SHAPE"), (dict(page_size=48), "UNSUPPORTED_SHAPE"),
               (dict(page_size=8192), "UNSUPPORTED_SHAPE"), (dict(bits_k=3), "UNSUPPORTED_SHAPE"),
               (dict(bits_v=0), "UNSUPPORTED_SHAPE"), (dict(bits_v=16), "UNSUPPORTED_SHAPE"),
+              (dict(n_pages=1 << 24), "UNSUPPORTED_SHAPE"),
               (dict(n_heads=0), "INVALID_ARG"), (dict(n_pages=0), "INVALID_ARG"), (dict(k_codes=0), "INVALID_ARG"),
               (dict(v_scales=0), "INVALID_ARG"), (dict(k_scales=PTR + 4), "INVALID_ARG"),
               (dict(v_codes=PTR + 8), "INVALID_ARG")]

@@ -1,4 +1,5 @@
-// Attention of a few rows per KV head (up to 32: single tokens, small trees) over the paged cache.
+// Attention of a few rows per KV head (more than the codes' kernel takes, up to 32: small trees) over the
+// paged cache.
 //
 // For a new row at position p_q of a sequence, over the keys it sees,
 //   s_t = cap tanh(scale (q . k_t) / cap) - slope (p_q - p_t),   o = sum_t softmax(s)_t v_t,

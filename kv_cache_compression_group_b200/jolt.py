@@ -7,6 +7,8 @@ raises if the library is missing: there is no other implementation behind it.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from dataclasses import dataclass
 
@@ -153,6 +155,43 @@ def _stream(stream=None):
 
 def _ptr(t):
     return ctypes.c_void_p(0 if t is None else t.data_ptr())
+
+
+def _torch_stream(stream, device):
+    """A stream argument (a torch stream, another object with a cuda_stream, or a raw handle) as a torch stream."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+        # 1 is the legacy default stream's other name
+        return torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream must be on device {device}")
+    return stream
+
+
+def _on_its_stream(f):
+    """A call that is given a stream runs whole on it, as under torch.cuda.stream(stream).  The device is
+    that of the call's first argument: its object, or a tensor.
+
+    The kernels alone would not do: torch's allocator hands freed memory on at once, ordered on the stream
+    that it was allocated on, so a buffer taken on the current stream may still be in use there by a call
+    that has returned, and what is filled or converted on the current stream is not waited for.  Results
+    are marked as used by the caller's current stream too."""
+    place = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = kw.pop("stream", None) if len(args) <= place else args[place]
+        if stream is None:
+            return f(*args[:place], **kw)
+        device = args[0].device
+        before = torch.cuda.current_stream(device)
+        with torch.cuda.stream(_torch_stream(stream, device)):
+            result = f(*args[:place], **kw)
+        for t in result if isinstance(result, tuple) else (result,):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(before)
+        return result
+    return call
 
 
 # ------------------------------------------------------------------------------------------
@@ -420,7 +459,10 @@ class QuantCache:
     codes uint8 [n_layers, n_pages, n_heads, page_size, head_dim * bits / 8], scales fp16
     [n_layers, n_pages, n_heads, page_size, head_dim / 16, 2].  bits: of K and V, each 2, 4 or 8.
     The errors that only the device sees (a batch naming rows or pages that do not exist, NaN
-    among the rows) collect in a status word that check() reads."""
+    among the rows) collect in a status word that check() reads.
+
+    stream (of every call): a torch stream or a raw handle to run on instead of the current stream; what
+    the call is given has to be ready there, and its results are.  They come from that stream's memory."""
 
     def __init__(self, n_layers, n_heads, head_dim, n_pages, page_size=64, bits=(4, 4), device="cuda", pools=None):
         bits = (bits, bits) if isinstance(bits, int) else tuple(bits)
@@ -462,13 +504,10 @@ class QuantCache:
         _check(lib().jolt_cache_attend_scratch_size(c, b, nq, ctypes.byref(nbytes)))
         return nbytes.value
 
-    def _run(self, call, stream, *args):
-        """call(*args, stream) on the cache's device: on the given stream, else on the current one."""
+    def _run(self, call, *args):
+        """call(*args, stream) on the cache's device and its current stream."""
         idx = self.device.index
-        if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(idx)
-        elif hasattr(stream, "cuda_stream"):
-            stream = stream.cuda_stream
+        stream = torch._C._cuda_getCurrentRawStream(idx)
         if torch.cuda.current_device() == idx:
             status = call(*args, stream)
         else:
@@ -499,6 +538,7 @@ class QuantCache:
             raise ValueError(f"the features of {name} must be contiguous")
         return row, head
 
+    @_on_its_stream
     def write(self, layer: int, k: torch.Tensor, v: torch.Tensor, batch: CacheBatch, stream=None):
         """Quantise rows k, v [rows, n_heads, head_dim] (bf16, fp16 or fp32, strided rows and heads)
         into their pages: they become the last rows of the batch's sequences."""
@@ -507,8 +547,9 @@ class QuantCache:
         if k.dtype != v.dtype or k.shape != v.shape or k.dtype not in _CACHE_DTYPES:
             raise ValueError("k and v must have one shape and one of the types bf16, fp16, fp32")
         c, b = self._call(layer, batch, k.shape[0], k, v)
-        self._run(lib().jolt_cache_write, stream, c, b, k.data_ptr(), v.data_ptr(), _CACHE_DTYPES[k.dtype], *ks, *vs)
+        self._run(lib().jolt_cache_write, c, b, k.data_ptr(), v.data_ptr(), _CACHE_DTYPES[k.dtype], *ks, *vs)
 
+    @_on_its_stream
     def read(self, layer: int, batch: CacheBatch, rows: int, dtype=torch.bfloat16, out=None, stream=None):
         """The batch's rows as dense (k, v), each [rows, n_heads, head_dim] of dtype; out: tensors to
         write into (rows that belong to no sequence are left as they are)."""
@@ -523,9 +564,10 @@ class QuantCache:
         if k.dtype != dtype or v.dtype != dtype or k.shape != v.shape or k.shape[0] != rows:
             raise ValueError("out must be two tensors of dtype and rows")
         c, b = self._call(layer, batch, k.shape[0], k, v)
-        self._run(lib().jolt_cache_read, stream, c, b, _CACHE_DTYPES[dtype], k.data_ptr(), v.data_ptr(), *ks, *vs)
+        self._run(lib().jolt_cache_read, c, b, _CACHE_DTYPES[dtype], k.data_ptr(), v.data_ptr(), *ks, *vs)
         return k, v
 
+    @_on_its_stream
     def attend(self, layer: int, q: torch.Tensor, batch: CacheBatch, scale: float = 0.0, softcap: float = 0.0,
                window: int = 0, slopes=None, positions=None, mask=None, prefix=None, out=None, stream=None):
         """Attention of rows q [rows, n_q_heads, head_dim] (bf16 or fp16), whose keys and values are
@@ -552,13 +594,12 @@ class QuantCache:
             out = torch.empty((rows, nq, self.head_dim), dtype=q.dtype, device=self.device)
         elif out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("out must have q's shape and type")
-        # a scratch of its own for every call: two calls, or two captured graphs, never share one
+        # a scratch of its own for every call, from the pool of the stream that it runs on: a later call
+        # can only get it behind this one, and two captured graphs with pools of their own never share one
         nbytes = self._scratch_bytes(c, b, nq)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        self._run(lib().jolt_cache_attend, stream, c, b, o, q.data_ptr(), _CACHE_DTYPES[q.dtype], nq, *qs,
+        self._run(lib().jolt_cache_attend, c, b, o, q.data_ptr(), _CACHE_DTYPES[q.dtype], nq, *qs,
                   out.data_ptr(), *self._rows(out, "out", nq), scratch.data_ptr(), nbytes)
-        if isinstance(stream, torch.cuda.Stream):
-            scratch.record_stream(stream)
         return out
 
     def _extras(self, o, rows, nq, slopes, positions, mask, prefix):
@@ -581,10 +622,11 @@ class QuantCache:
                 raise ValueError("mask must be [rows, words]")
             o.mask_words = mask.shape[1]
 
+    @_on_its_stream
     def check(self, stream=None):
         """Raise what the kernels of this cache's calls found so far (synchronises), and clear it."""
         try:
-            self._run(lib().jolt_cache_check, stream, self._status_ptr)
+            self._run(lib().jolt_cache_check, self._status_ptr)
         except JoltError:
             self.status.zero_()
             raise

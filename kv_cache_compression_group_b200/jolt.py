@@ -169,24 +169,34 @@ def _torch_stream(stream, device):
 
 
 def _on_its_stream(f):
-    """A call that is given a stream runs whole on it, as under torch.cuda.stream(stream).  The device is
-    that of the call's first argument: its object, or a tensor.
+    """A call that is given a stream runs whole on it, as under torch.cuda.stream(stream); one that is not
+    runs on the current stream of its device, that of its first argument (its object, or a tensor).
 
     The kernels alone would not do: torch's allocator hands freed memory on at once, ordered on the stream
     that it was allocated on, so a buffer taken on the current stream may still be in use there by a call
     that has returned, and what is filled or converted on the current stream is not waited for.  Results
     are marked as used by the caller's current stream too."""
-    place = list(inspect.signature(f).parameters).index("stream")
+    names = list(inspect.signature(f).parameters)
+    place = names.index("stream")
 
     @functools.wraps(f)
     def call(*args, **kw):
         stream = kw.pop("stream", None) if len(args) <= place else args[place]
+        args = args[:place]
+        device = (args[0] if args else kw[names[0]]).device
+        if device.type != "cuda":                       # f refuses what is not on a GPU
+            return f(*args, **kw)
+        current = torch.cuda.current_device()
         if stream is None:
-            return f(*args[:place], **kw)
-        device = args[0].device
+            if device.index is None or device.index == current:
+                return f(*args, **kw)
+            with torch.cuda.device(device):
+                return f(*args, **kw)
+        if device.index is None:
+            device = torch.device("cuda", current)
         before = torch.cuda.current_stream(device)
         with torch.cuda.stream(_torch_stream(stream, device)):
-            result = f(*args[:place], **kw)
+            result = f(*args, **kw)
         for t in result if isinstance(result, tuple) else (result,):
             if isinstance(t, torch.Tensor):
                 t.record_stream(before)
@@ -305,6 +315,7 @@ class Compressor:
         p = t.data_ptr()
         return ctypes.c_void_p((p + 255) // 256 * 256)
 
+    @_on_its_stream
     def compress(self, K, V, budget: int, seed: int = 0, blob: torch.Tensor | None = None, stream=None):
         """Compress K, V under `budget` total bytes; returns the blob (uint8 device tensor of
         capacity max(budget, needed)).  Asynchronous; errors found on the device surface in
@@ -315,9 +326,10 @@ class Compressor:
             blob = torch.empty(max(cap, 64 + 64 * self.n_units), dtype=torch.uint8, device=K.device)
         _check(lib().jolt_compress(ctypes.byref(self.shape), _ptr(K), _ptr(V), ctypes.byref(self._copts),
                                    int(budget), int(seed), _ptr(blob), blob.numel(), self._ws_ptr(self.ws),
-                                   self.ws_bytes, _stream(stream)))
+                                   self.ws_bytes, _stream()))
         return blob
 
+    @_on_its_stream
     def factor(self, K, V, seed: int = 0, stream=None):
         _check_cache(K, V)
         o = self.opts
@@ -325,9 +337,10 @@ class Compressor:
         U = torch.zeros((self.n_units, self.shape.n_tokens, rT), dtype=torch.float32, device=K.device)
         W = torch.zeros((self.n_units, self.shape.head_dim, rD), dtype=torch.float32, device=K.device)
         _check(lib().jolt_factor(ctypes.byref(self.shape), _ptr(K), _ptr(V), ctypes.byref(self._copts), int(seed),
-                                 _ptr(U), rT, _ptr(W), rD, self._ws_ptr(self.ws), self.ws_bytes, _stream(stream)))
+                                 _ptr(U), rT, _ptr(W), rD, self._ws_ptr(self.ws), self.ws_bytes, _stream()))
         return U, W
 
+    @_on_its_stream
     def table(self, K, V, U_bf16, W_bf16, seed: int = 0, stream=None):
         """Core (bf16) and distortion table (fp64) from given bf16 factors [units, T, r_T], [units, D, r_D]."""
         _check_cache(K, V)
@@ -340,9 +353,10 @@ class Compressor:
         W_bf16 = W_bf16.contiguous()
         _check(lib().jolt_table(ctypes.byref(self.shape), _ptr(K), _ptr(V), ctypes.byref(self._copts), int(seed),
                                 _ptr(U_bf16), U_bf16.shape[-1], _ptr(W_bf16), W_bf16.shape[-1], _ptr(core),
-                                _ptr(tab), self._ws_ptr(self.ws), self.ws_bytes, _stream(stream)))
+                                _ptr(tab), self._ws_ptr(self.ws), self.ws_bytes, _stream()))
         return core, tab
 
+    @_on_its_stream
     def recon_operator(self, core, W_bf16, seed: int = 0, stream=None):
         """Rotated reconstruction operators P' [n_feature_ranks, units, S, max r_T, D] (bf16)."""
         o = self.opts
@@ -352,9 +366,10 @@ class Compressor:
         W_bf16 = W_bf16.contiguous()
         _check(lib().jolt_recon_operator(ctypes.byref(self.shape), ctypes.byref(self._copts), int(seed),
                                          _ptr(core.contiguous()), _ptr(W_bf16), W_bf16.shape[-1], _ptr(P),
-                                         self._ws_ptr(self.ws), self.ws_bytes, _stream(stream)))
+                                         self._ws_ptr(self.ws), self.ws_bytes, _stream()))
         return P
 
+    @_on_its_stream
     def encode(self, K, V, U_bf16, W_bf16, core, choice, dist, seed: int = 0, cap: int | None = None, stream=None):
         _check_cache(K, V)
         cap = self.blob_max if cap is None else cap
@@ -364,9 +379,10 @@ class Compressor:
         _check(lib().jolt_encode(ctypes.byref(self.shape), _ptr(K), _ptr(V), ctypes.byref(self._copts), int(seed),
                                  _ptr(U_bf16.contiguous()), U_bf16.shape[-1], _ptr(W_bf16.contiguous()),
                                  W_bf16.shape[-1], _ptr(core.contiguous()), _ptr(choice), _ptr(dist), _ptr(blob),
-                                 blob.numel(), self._ws_ptr(self.ws), self.ws_bytes, _stream(stream)))
+                                 blob.numel(), self._ws_ptr(self.ws), self.ws_bytes, _stream()))
         return blob
 
+    @_on_its_stream
     def decompress(self, blob, out_dtype=None, K_out=None, V_out=None, stream=None):
         if out_dtype is None:
             out_dtype = torch.bfloat16 if self.shape.dtype == JOLT_BF16 else torch.float32
@@ -378,7 +394,7 @@ class Compressor:
             self.dws = torch.empty(self.dws_bytes + 256, dtype=torch.uint8, device=blob.device)
         _check(lib().jolt_decompress(_ptr(blob), JOLT_F32 if out_dtype == torch.float32 else JOLT_BF16,
                                      _ptr(K_out), _ptr(V_out), self._ws_ptr(self.dws), self.dws_bytes,
-                                     _stream(stream)))
+                                     _stream()))
         return K_out, V_out
 
 
@@ -388,40 +404,48 @@ class Attention:
 
     def __init__(self, comp: "Compressor", blob: torch.Tensor, n_q_heads: int, stream=None):
         self.blob = blob
+        self.device = blob.device
         self.nq = int(n_q_heads)
         self.D = comp.shape.head_dim
-        self.ws = torch.empty(comp.dws_bytes + 256, dtype=torch.uint8, device=blob.device)
-        self.ws_ptr = comp._ws_ptr(self.ws)
-        self.ws_bytes = comp.dws_bytes
         nbytes = ctypes.c_size_t()
         _check(lib().jolt_attend_scratch_size(ctypes.byref(comp.shape), max(comp.opts.token_ranks), self.nq,
                                               ctypes.byref(nbytes)))
-        self.scratch = torch.empty(nbytes.value, dtype=torch.uint8, device=blob.device)
-        _check(lib().jolt_attend_prepare(_ptr(blob), self.ws_ptr, self.ws_bytes, _stream(stream)))
+        self.scratch_bytes = nbytes.value
+        self._prepare(comp, stream=stream)
 
-    def attend(self, layer: int, q: torch.Tensor, out: torch.Tensor | None = None, stream=None):
-        """q [n_q_heads, head_dim] fp32 on the device; returns the attention output (same shape)."""
+    @_on_its_stream
+    def _prepare(self, comp, stream=None):
+        self.ws = torch.empty(comp.dws_bytes + 256, dtype=torch.uint8, device=self.device)
+        self.ws_ptr = comp._ws_ptr(self.ws)
+        self.ws_bytes = comp.dws_bytes
+        _check(lib().jolt_attend_prepare(_ptr(self.blob), self.ws_ptr, self.ws_bytes, _stream()))
+
+    def _run(self, layer, q, out, lse):
         q = q.to(torch.float32).contiguous()
         if q.shape != (self.nq, self.D):
             raise ValueError(f"q must be [{self.nq}, {self.D}]")
         if out is None:
             out = torch.empty_like(q)
-        _check(lib().jolt_attend(_ptr(self.blob), self.ws_ptr, self.ws_bytes, int(layer), _ptr(q), self.nq, _ptr(out),
-                                 _ptr(self.scratch), self.scratch.numel(), _stream(stream)))
+        # a scratch of its own for every call: two calls on two streams do not share one
+        args = (_ptr(self.blob), self.ws_ptr, self.ws_bytes, int(layer), _ptr(q), self.nq, _ptr(out))
+        scratch = torch.empty(self.scratch_bytes, dtype=torch.uint8, device=self.device)
+        if lse is None:
+            _check(lib().jolt_attend(*args, _ptr(scratch), self.scratch_bytes, _stream()))
+        else:
+            _check(lib().jolt_attend_state(*args, _ptr(lse), _ptr(scratch), self.scratch_bytes, _stream()))
         return out
 
+    @_on_its_stream
+    def attend(self, layer: int, q: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+        """q [n_q_heads, head_dim] fp32 on the device; returns the attention output (same shape)."""
+        return self._run(layer, q, out, None)
+
+    @_on_its_stream
     def attend_state(self, layer: int, q: torch.Tensor, stream=None):
         """As attend, with the log-sum-exp of the scores: (output, lse [n_q_heads] fp32), the prefix
         that QuantCache.attend joins to its own keys."""
-        q = q.to(torch.float32).contiguous()
-        if q.shape != (self.nq, self.D):
-            raise ValueError(f"q must be [{self.nq}, {self.D}]")
-        out = torch.empty_like(q)
-        lse = torch.empty(self.nq, dtype=torch.float32, device=q.device)
-        _check(lib().jolt_attend_state(_ptr(self.blob), self.ws_ptr, self.ws_bytes, int(layer), _ptr(q), self.nq,
-                                       _ptr(out), _ptr(lse), _ptr(self.scratch), self.scratch.numel(),
-                                       _stream(stream)))
-        return out, lse
+        lse = torch.empty(self.nq, dtype=torch.float32, device=self.device)
+        return self._run(layer, q, None, lse), lse
 
 
 _CACHE_DTYPES = {torch.bfloat16: JOLT_BF16, torch.float32: JOLT_F32, torch.float16: JOLT_F16}
@@ -505,14 +529,8 @@ class QuantCache:
         return nbytes.value
 
     def _run(self, call, *args):
-        """call(*args, stream) on the cache's device and its current stream."""
-        idx = self.device.index
-        stream = torch._C._cuda_getCurrentRawStream(idx)
-        if torch.cuda.current_device() == idx:
-            status = call(*args, stream)
-        else:
-            with torch.cuda.device(idx):
-                status = call(*args, stream)
+        """call(*args, stream) on the current stream."""
+        status = call(*args, torch._C._cuda_getCurrentRawStream(self.device.index))
         if status:
             _check(status)
 
@@ -632,6 +650,7 @@ class QuantCache:
             raise
 
 
+@_on_its_stream
 def read_header(blob: torch.Tensor, stream=None):
     """(shape dict, total bytes, list of unit records); synchronises.  Raises on a device-side
     error recorded in the blob (infeasible budget, non-finite input, ...)."""
@@ -639,7 +658,7 @@ def read_header(blob: torch.Tensor, stream=None):
     tot = ctypes.c_uint64()
     n = 4096
     recs = (CUnitRecord * n)()
-    _check(lib().jolt_read_header(_ptr(blob), ctypes.byref(sh), ctypes.byref(tot), recs, n, _stream(stream)))
+    _check(lib().jolt_read_header(_ptr(blob), ctypes.byref(sh), ctypes.byref(tot), recs, n, _stream()))
     G = sh.n_layers // sh.layers_per_group
     units = [dict(r_T=r.r_T, r_D=r.r_D, bits=r.bits, choice=r.choice, off_U=r.off_U, off_W=r.off_W,
                   off_C=r.off_C, off_codes=r.off_codes, off_scales=r.off_scales, distortion=r.distortion)
@@ -649,6 +668,7 @@ def read_header(blob: torch.Tensor, stream=None):
     return shape, tot.value, units
 
 
+@_on_its_stream
 def allocate(dist: torch.Tensor, nbytes: torch.Tensor, budget: int, stream=None):
     """Lagrangian dual on device tables [units, choices]: returns (choice int32, lambda, status)."""
     nu, nc = dist.shape
@@ -658,10 +678,11 @@ def allocate(dist: torch.Tensor, nbytes: torch.Tensor, budget: int, stream=None)
     lam = torch.zeros(1, dtype=torch.float64, device=dist.device)
     status = torch.zeros(1, dtype=torch.int32, device=dist.device)
     _check(lib().jolt_allocate(_ptr(dist), _ptr(nbytes), nu, nc, int(budget), _ptr(choice), _ptr(lam), _ptr(status),
-                               _stream(stream)))
+                               _stream()))
     return choice, lam, status
 
 
+@_on_its_stream
 def frobenius(K, V, K_hat=None, V_hat=None, layers_per_group=1, stream=None):
     """Per-unit [||X_u||^2, ||X_u - Y_u||^2] (fp64, device) for units u = 2 g + kv."""
     shape = make_shape(K, layers_per_group)
@@ -670,7 +691,7 @@ def frobenius(K, V, K_hat=None, V_hat=None, layers_per_group=1, stream=None):
     ws = torch.empty(2 * G * 64 * 16, dtype=torch.uint8, device=K.device)
     yd = JOLT_F32 if (K_hat is not None and K_hat.dtype == torch.float32) else JOLT_BF16
     _check(lib().jolt_frobenius(ctypes.byref(shape), _ptr(K), _ptr(V), _ptr(K_hat), _ptr(V_hat), yd, _ptr(sq),
-                                _ptr(ws), ws.numel(), _stream(stream)))
+                                _ptr(ws), ws.numel(), _stream()))
     return sq.view(2 * G, 2)
 
 
@@ -718,6 +739,7 @@ def wait_selftest(arrive: bool, limit_us: int, status: torch.Tensor, stream=None
     _check(lib().jolt_wait_selftest(1 if arrive else 0, int(limit_us), _ptr(status), _stream(stream)))
 
 
+@_on_its_stream
 def frobenius_noalloc(K, V, K_hat=None, V_hat=None, layers_per_group=1, stream=None):
     """As frobenius(), through the entry point that needs no workspace (its scratch is a
     fixed array inside the library; calls whose GPU work overlaps must not be mixed)."""
@@ -726,10 +748,11 @@ def frobenius_noalloc(K, V, K_hat=None, V_hat=None, layers_per_group=1, stream=N
     sq = torch.zeros(2 * 2 * G, dtype=torch.float64, device=K.device)
     yd = JOLT_F32 if (K_hat is not None and K_hat.dtype == torch.float32) else JOLT_BF16
     _check(lib().jolt_frobenius_noalloc(ctypes.byref(shape), _ptr(K), _ptr(V), _ptr(K_hat), _ptr(V_hat), yd,
-                                        _ptr(sq), _stream(stream)))
+                                        _ptr(sq), _stream()))
     return sq.view(2 * G, 2)
 
 
+@_on_its_stream
 def quant_baseline(K, V, bits: int, layers_per_group: int, keep_codes: bool = False, stream=None):
     """Per-block b-bit quantisation of K and V themselves: per-unit [||X_u||^2, ||X_u - Q(X_u)||^2]
     (fp64, device), and (keep_codes) the codes and fp16 scales."""
@@ -741,7 +764,7 @@ def quant_baseline(K, V, bits: int, layers_per_group: int, keep_codes: bool = Fa
     codes = torch.empty(nblk_all * 2 * bits, dtype=torch.uint8, device=K.device) if keep_codes else None
     scales = torch.empty(nblk_all * 2, dtype=torch.float16, device=K.device) if keep_codes else None
     _check(lib().jolt_quant_baseline(ctypes.byref(shape), _ptr(K), _ptr(V), int(bits), _ptr(codes), _ptr(scales),
-                                     _ptr(sq), _ptr(ws), ws.numel(), _stream(stream)))
+                                     _ptr(sq), _ptr(ws), ws.numel(), _stream()))
     return sq.view(2 * G, 2), codes, scales
 
 

@@ -356,8 +356,8 @@ typedef struct {
  * those new rows that its mask allows, both inside the window; query head j reads KV head
  * j / (n_q_heads / n_heads).  o = sum_t p_t v_t with p the softmax of s; a row that sees nothing
  * gives its prefix, or zeros.  The weights p enter the products as fp16, and with more than a few
- * rows per KV head the stored values too (one rounding of lo + code * step); sums, maxima and the
- * softmax are fp32.
+ * rows per KV head the stored values too (lo + code * step off by at most 2^-11 of itself and 2^-23);
+ * sums, maxima and the softmax are fp32.
  *   q_dev   : [n_rows][n_q_heads][head_dim] of `dtype` (JOLT_BF16 or JOLT_F16), strides in elements
  *   out_dev : the same shape and type, its own strides
  *   scratch_dev: jolt_cache_attend_scratch_size bytes, 256-byte aligned, contents irrelevant; two

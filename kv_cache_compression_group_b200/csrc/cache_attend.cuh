@@ -17,8 +17,10 @@
 //     packed words of D / 4 consecutive features, and Q^T is laid out to match once per job;
 //   * V's fragment pairs two tokens of one feature.  ldmatrix.trans transposes 16-bit units, here
 //     16 / bits codes of one token, so one shift and mask of its result gives the pair.
-// A value is fp16(lo / 2 + code * (step / 2)): one rounding, and halves so that the top of fp16's
-// range does not overflow; the factor returns in fp32.
+// A value is fp16(lo / 2 + step * (code / 2)): one rounding, of halves so that the top of fp16's range does
+// not overflow; the factor returns in fp32.  The half is the code's, which is exact (half a step would lose
+// a bit below 2^-13, times a code of up to 255: 6e-3 of 8-bit values of 1e-3, their quantiser 4e-3); only lo / 2 may
+// lose its last bit, below 2^-13, so a value is off by at most 2^-11 of itself and 2^-23.
 #pragma once
 
 #include "cache_split.cuh"
@@ -62,11 +64,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ uint32_t h2u(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ __half2 u2h(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
-// The exponent of 1024 in both halves, in a register the compiler cannot see through: with it, mask
+// The exponent of 512 in both halves, in a register the compiler cannot see through: with it, mask
 // and exponent go in by one three-input logic operation (as two immediates they would take two).
-__device__ __forceinline__ uint32_t magic1024() {
+__device__ __forceinline__ uint32_t magic512() {
   uint32_t x;
-  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(x));
+  asm volatile("mov.b32 %0, 0x60006000;" : "=r"(x));
   return x;
 }
 __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t magic) {
@@ -75,25 +77,25 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t m
   return y;
 }
 
-// Codes s of the two 16-bit halves of w as an fp16 pair: the code under the exponent of 1024
-// (or of 1024 with the code 4^k times too large, where it is not shifted down), made exact by one
-// subtraction (or fused multiply-add).
+// Half of codes s of the two 16-bit halves of w as an fp16 pair: the code under the exponent of 512,
+// where fp16's step is 1/2 (or there with the code 4^k times too large, where it is not shifted down),
+// made exact by one subtraction (or fused multiply-add).
 template <int BITS>
-__device__ __forceinline__ __half2 code_pair(uint32_t w, int s, uint32_t magic) {
-  const __half2 k1024 = __float2half2_rn(-1024.f);
+__device__ __forceinline__ __half2 half_code_pair(uint32_t w, int s, uint32_t magic) {
+  const __half2 k512 = __float2half2_rn(-512.f);
   if constexpr (BITS == 2) {
     const uint32_t v = s < 4 ? w : w >> 8;
     const int p = 2 * (s & 3);
     const uint32_t x = and_or(v, 0x00030003u << p, magic);
-    if (p == 0) return __hadd2(u2h(x), k1024);
+    if (p == 0) return __hadd2(u2h(x), k512);
     const float f = 1.f / (float)(1 << p);
-    return __hfma2(u2h(x), __float2half2_rn(f), __float2half2_rn(-1024.f * f));
+    return __hfma2(u2h(x), __float2half2_rn(f), __float2half2_rn(-512.f * f));
   } else if constexpr (BITS == 4) {
     const uint32_t v = s < 2 ? w : w >> 8;
-    if ((s & 1) == 0) return __hadd2(u2h(and_or(v, 0x000f000fu, magic)), k1024);
-    return __hfma2(u2h(and_or(v, 0x00f000f0u, magic)), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
+    if ((s & 1) == 0) return __hadd2(u2h(and_or(v, 0x000f000fu, magic)), k512);
+    return __hfma2(u2h(and_or(v, 0x00f000f0u, magic)), __float2half2_rn(0.0625f), __float2half2_rn(-32.f));
   } else {
-    return __hadd2(u2h(__byte_perm(w, magic, s == 0 ? 0x5250 : 0x5351)), k1024);
+    return __hadd2(u2h(__byte_perm(w, magic, s == 0 ? 0x5250 : 0x5351)), k512);
   }
 }
 
@@ -153,7 +155,7 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], uint32_t kc, uint32_t 
       sc[t][0] = u2h(v);
     }
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) sc[t][i] = __hmul2(sc[t][i], __float2half2_rn(0.5f));
+    for (int i = 0; i < D / 64; ++i) sc[t][i] = __hmul2(sc[t][i], __floats2half2_rn(0.5f, 1.f));
   }
   constexpr int PER = 32 / BITS;
 #pragma unroll
@@ -164,7 +166,7 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], uint32_t kc, uint32_t 
     for (int t = 0; t < 2; ++t) {
       const __half2 lo = __low2half2(sc[t][blk]), step = __high2half2(sc[t][blk]);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) a[t][r] = h2u(__hfma2(code_pair<BITS>(w[t][word], pair + r, magic), step, lo));
+      for (int r = 0; r < 2; ++r) a[t][r] = h2u(__hfma2(half_code_pair<BITS>(w[t][word], pair + r, magic), step, lo));
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -194,8 +196,8 @@ __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], uint32_t vc, u
       ldsm2t(sc[0], sc[1], vsc + row * 16);
     }
 #pragma unroll
-    for (int i = 0; i < 2 * SCH; ++i)
-      sc[i] = h2u(__hmul2(u2h(sc[i]), __float2half2_rn(0.5f))) & ((i & 1) ? live1 : live0);
+    for (int i = 0; i < 2 * SCH; ++i)      // lanes of even columns g hold lo, of odd ones step
+      sc[i] = h2u(__hmul2(u2h(sc[i]), __float2half2_rn(g & 1 ? 1.f : 0.5f))) & ((i & 1) ? live1 : live0);
   }
 #pragma unroll
   for (int q2 = 0; q2 < CH; q2 += 2) {
@@ -214,10 +216,10 @@ __device__ __forceinline__ void values(float (&o)[NT][D / 16][4], uint32_t vc, u
       const __half2 st1 = u2h(__shfl_sync(0xffffffffu, sc[2 * z + 1], src + 4));
 #pragma unroll
       for (int sp = 0; sp < CPU / 2; ++sp) {
-        const uint32_t a0 = h2u(__hfma2(code_pair<BITS>(r[2 * u], 2 * sp, magic), st0, lo0));
-        const uint32_t a1 = h2u(__hfma2(code_pair<BITS>(r[2 * u], 2 * sp + 1, magic), st0, lo0));
-        const uint32_t a2 = h2u(__hfma2(code_pair<BITS>(r[2 * u + 1], 2 * sp, magic), st1, lo1));
-        const uint32_t a3 = h2u(__hfma2(code_pair<BITS>(r[2 * u + 1], 2 * sp + 1, magic), st1, lo1));
+        const uint32_t a0 = h2u(__hfma2(half_code_pair<BITS>(r[2 * u], 2 * sp, magic), st0, lo0));
+        const uint32_t a1 = h2u(__hfma2(half_code_pair<BITS>(r[2 * u], 2 * sp + 1, magic), st0, lo0));
+        const uint32_t a2 = h2u(__hfma2(half_code_pair<BITS>(r[2 * u + 1], 2 * sp, magic), st1, lo1));
+        const uint32_t a3 = h2u(__hfma2(half_code_pair<BITS>(r[2 * u + 1], 2 * sp + 1, magic), st1, lo1));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][qc * (CPU / 2) + sp], a0, a1, a2, a3, p[nt][0], p[nt][1]);
       }
@@ -369,7 +371,7 @@ __device__ __forceinline__ void few_loop(const CacheAttendArgs& A, const FewJob<
   constexpr int STAGE = KBYTES + VBYTES + 2 * SBYTES, KCH = D * KB / 128, VCH = D * VB / 128, SCH = D / 64;
   const int g = lane >> 2, c = lane & 3, len = J.len, old = J.len - J.n, count = J.count, tw = J.tw;
   const bool plain = A.cap == 0.f;
-  const uint32_t magic = magic1024(), ring = smem_addr(mine);
+  const uint32_t magic = magic512(), ring = smem_addr(mine);
   const uint32_t kdst = swizzled<KCH>(lane / KCH, lane % KCH), vdst = KBYTES + SBYTES + swizzled<VCH>(lane / VCH, lane % VCH);
   const uint32_t ksd = KBYTES + swizzled<SCH>(lane / SCH, lane % SCH), vsd = ksd + SBYTES + VBYTES;
   const unsigned char* kc = A.c.codes[0] + lane * 16;

@@ -5,7 +5,7 @@
 // in tiles of 128 tokens.  One persistent CTA of 20 warps per SM:
 //   * one warp walks the tiles and looks up their pages, several tiles ahead;
 //   * eight dequantising warps take 16 tokens of every tile each: packed codes and (lo, step) pairs
-//     straight to registers, one tile ahead, then fp16(lo / 2 + code * (step / 2)) into the
+//     straight to registers, one tile ahead, then fp16(lo / 2 + step * (code / 2)) into the
 //     128-byte-swizzled operand tiles, two of K and two of V.  The features of a row keep the order
 //     in which a packed word gives its pairs; Q is laid out in the same order, the output columns
 //     are put back;
@@ -344,10 +344,10 @@ __device__ __forceinline__ void raw_store(const RawRegs& r, uint32_t tile, int r
     uint32_t h[4 * PER / 2];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const __half2 sc = __hmul2(ca::u2h(r.scale[i * W::BLKS + k * PER / 16]), __float2half2_rn(0.5f));
+      const __half2 sc = __hmul2(ca::u2h(r.scale[i * W::BLKS + k * PER / 16]), __floats2half2_rn(0.5f, 1.f));
       const __half2 lo = __low2half2(sc), step = __high2half2(sc);
 #pragma unroll
-      for (int p = 0; p < PER / 2; ++p) h[k * PER / 2 + p] = ca::h2u(__hfma2(ca::code_pair<BITS>(words[k], p, magic), step, lo));
+      for (int p = 0; p < PER / 2; ++p) h[k * PER / 2 + p] = ca::h2u(__hfma2(ca::half_code_pair<BITS>(words[k], p, magic), step, lo));
     }
 #pragma unroll
     for (int k = 0; k < 4 * PER / 8; ++k)
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(ct::THREADS, 1) cache_many_rows_kernel(CacheAt
     // ================= dequantising warps =================
     regs_down<DEQUANT_REGS>();
     const int grp = warp - 8;                  // tokens 16 grp .. + 15 of every tile
-    const uint32_t magic = ca::magic1024();
+    const uint32_t magic = ca::magic512();
     const unsigned char* const kc = A.c.codes[0];
     const unsigned char* const vc = A.c.codes[1];
     const __half2* const ks = A.c.scales[0];

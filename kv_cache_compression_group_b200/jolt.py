@@ -182,18 +182,16 @@ def _on_its_stream(f):
     @functools.wraps(f)
     def call(*args, **kw):
         stream = kw.pop("stream", None) if len(args) <= place else args[place]
-        args = args[:place]
         device = (args[0] if args else kw[names[0]]).device
-        if device.type != "cuda":                       # f refuses what is not on a GPU
-            return f(*args, **kw)
-        current = torch.cuda.current_device()
+        index = device.index                            # None: the current device's, or not on a GPU (f refuses it)
         if stream is None:
-            if device.index is None or device.index == current:
+            if index is None or index == torch.cuda.current_device():
                 return f(*args, **kw)
             with torch.cuda.device(device):
                 return f(*args, **kw)
-        if device.index is None:
-            device = torch.device("cuda", current)
+        args = args[:place]
+        if index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
         before = torch.cuda.current_stream(device)
         with torch.cuda.stream(_torch_stream(stream, device)):
             result = f(*args, **kw)

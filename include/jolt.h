@@ -355,9 +355,10 @@ typedef struct {
  * already written (they are the last n_b of lens[b]).  A row sees the keys before the new rows and
  * those new rows that its mask allows, both inside the window; query head j reads KV head
  * j / (n_q_heads / n_heads).  o = sum_t p_t v_t with p the softmax of s; a row that sees nothing
- * gives its prefix, or zeros.  The weights p enter the products as fp16, and with more than a few
- * rows per KV head the stored values too (lo + code * step off by at most 2^-11 of itself and 2^-23);
- * sums, maxima and the softmax are fp32.
+ * gives its prefix, or zeros.  The weights p enter the products as fp16.  With more than a few rows per
+ * KV head the stored values do too (lo + code * step off by at most 2^-11 of itself and 2^-23); with fewer
+ * it is the product of a weight and a step, off by another 2^-11 of itself (and nothing of the keys).
+ * Sums, maxima and the softmax are fp32.
  *   q_dev   : [n_rows][n_q_heads][head_dim] of `dtype` (JOLT_BF16 or JOLT_F16), strides in elements
  *   out_dev : the same shape and type, its own strides
  *   scratch_dev: jolt_cache_attend_scratch_size bytes, 256-byte aligned, contents irrelevant; two

@@ -14,8 +14,8 @@
 // with R rows in use, column n stands for row n % R and block n / R of the chunk.
 //   K: column n of Q^T is zero outside its block's features, so S^T's columns are the blocks' partial
 //      sums; each is multiplied by its token's step and the columns of a row are added.
-//   V: column n of P^T is p times its block's step; of an output row (a feature) only the columns of
-//      its block are read.
+//   V: column n of P^T is p times its block's step, rounded to fp16 once more; of an output row (a feature)
+//      only the columns of its block are read.
 // The sums with lo are one product more each: [tokens x blocks] lo with the blocks' sums of q (as two
 // fp16 numbers, the second what the first leaves), and lo^T with p.
 // Four rows at 4 bits (eight at 8, two at 2) fill one n-tile of eight columns; twice as many take two.
@@ -27,9 +27,15 @@ namespace jolt {
 namespace cc {
 // rows of an n-tile: the fewer the more blocks a chunk of K or V has
 __host__ __device__ constexpr int rows_of(int kb, int vb) { return kb == 2 || vb == 2 ? 2 : kb == 4 || vb == 4 ? 4 : 8; }
-// weights are 2^(s - m + SHIFT) <= 2^(SHIFT + LAG) = 2^11, so that times a step below 32 they stay in
-// fp16's range; larger steps are treated apart
-constexpr float SHIFT = cs::SHIFT, LAG = 4.f, BIG_STEP = 32.f, BIG_SCALE = 0x1p-11f;
+// Weights are 2^(s - m + SHIFT) <= 2^(SHIFT + LAG) = 2^11, so that times a step below 32 they stay in
+// fp16's range.  The steps of a block of features enter the products times a power of two, `up`, that keeps the
+// largest so far below 32 (a larger one lowers `up`, and what was summed with it): without it the products of
+// low weights and small steps would be subnormal (a weight of 2^-12 and steps of 4e-7 round to zero).  It is
+// lowered to where the largest is below 4, so that it seldom has to be again (to below 32: 55 us instead of 52 us
+// for the 40-head case), and together with the maximum, where the sums are rescaled anyway (on its own: 114 us
+// instead of 109 us for the ragged batch, which it takes without `up` too; the 40-head case takes 49 us without).
+constexpr float SHIFT = cs::SHIFT, LAG = 4.f, STEP_LIMIT = 32.f, UP_MOST = 0x1p15f;
+constexpr int UP_LEAST = -11;               // fp16's largest number times 2^-11 is below 32
 
 // codes s of the two halves of w, as 4^k 2^-24 times the code: k = factor of code_scale
 template <int BITS>
@@ -222,6 +228,12 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
     pq_max = __reduce_max_sync(0xffffffffu, pq_max);
     const int edge = A.window ? pq_max - A.window + 1 : 0;    // keys from here on are seen by the window
     float o[NT][D / 16][4], olo[NT][4], m_ref[NT][2], l[NT][2];
+    // `up` of block 4 z + g / 2 in lanes of odd g, which hold the steps; the others hold lo, which stays as it
+    // is.  o is as many times its sums.
+    uint32_t up[SCH];
+    const uint32_t limit = h2u(__float2half2_rn(g & 1 ? cc::STEP_LIMIT : INFINITY));
+#pragma unroll
+    for (int z = 0; z < SCH; ++z) up[z] = h2u(__float2half2_rn(g & 1 ? cc::UP_MOST : 1.f));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -360,8 +372,27 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
           for (int k = 0; k < 4; ++k)
             s[nt][k] = fmaf(-slope[nt][k & 1], (float)(pq[nt][k & 1] - (t0 + g + 8 * (k >> 1))), s[nt][k]);
       }
+      // ---- the values' (lo, step) as columns, tokens as pairs, the steps times `up` ----
+      auto load_scales = [&](uint32_t (&x)[2 * SCH]) {
+        if constexpr (SCH == 2) ldsm4t(x, sta + vs_at);
+        else ldsm2t(x[0], x[1], sta + vs_at);
+        if (t0 + TOK > len) {              // what lies behind the sequence may be anything
+          const int t = t0 + 2 * c;
+          const uint32_t live0 = (t < len ? 0xffffu : 0u) | (t + 1 < len ? 0xffff0000u : 0u);
+          const uint32_t live1 = (t + 8 < len ? 0xffffu : 0u) | (t + 9 < len ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int k = 0; k < 2 * SCH; ++k) x[k] &= (k & 1) ? live1 : live0;
+        }
+      };
+      uint32_t sc[2 * SCH];
+      load_scales(sc);
+#pragma unroll
+      for (int k = 0; k < 2 * SCH; ++k) sc[k] = h2u(__hmul2(u2h(sc[k]), u2h(up[k / 2])));
+      __half2 top = u2h(sc[0]);
+#pragma unroll
+      for (int k = 1; k < 2 * SCH; ++k) top = __hmax2(top, u2h(sc[k]));
       // ---- running softmax over the tokens ----
-      bool grow = false;
+      bool grow = !__hblt2(top, u2h(limit));
       float mx[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -371,6 +402,7 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
           grow |= mx[nt][k] > m_ref[nt][k] + cc::LAG;
         }
       if (__any_sync(0xffffffffu, grow)) {
+        float f[NT][2], fu[SCH];           // what the sums are multiplied by, for the maximum and for `up`
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -379,17 +411,40 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
 #pragma unroll
             for (int z = 4; z < 32; z <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, z));
             const float to = fmaxf(x, m_ref[nt][k]);
-            const float f = m_ref[nt][k] == -INFINITY ? 0.f : cs::ex2(m_ref[nt][k] - to);
+            f[nt][k] = m_ref[nt][k] == -INFINITY ? 0.f : cs::ex2(m_ref[nt][k] - to);
             m_ref[nt][k] = to;
-            l[nt][k] *= f;
-            olo[nt][k] *= f;
-            olo[nt][2 + k] *= f;
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) {
-              o[nt][mt][k] *= f;
-              o[nt][mt][2 + k] *= f;
-            }
+            l[nt][k] *= f[nt][k];
+            olo[nt][k] *= f[nt][k];
+            olo[nt][2 + k] *= f[nt][k];
           }
+        load_scales(sc);
+#pragma unroll
+        for (int z = 0; z < SCH; ++z) {
+          const float2 x = __half22float2(__hmax2(u2h(sc[2 * z]), u2h(sc[2 * z + 1])));
+          float most = g & 1 ? fmaxf(x.x, x.y) : 0.f, was = __low2float(u2h(up[z]));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          // the power of two that takes the largest into [2, 4)
+          const int e = max(cc::UP_LEAST, 1 - ((int)(__float_as_uint(most) >> 23) - 127));
+          const float to = most * was >= cc::STEP_LIMIT ? __uint_as_float((uint32_t)(e + 127) << 23) : was;
+          fu[z] = to * __uint_as_float(0x7f000000u - __float_as_uint(was));   // to / was
+          up[z] = h2u(__float2half2_rn(to));
+          sc[2 * z] = h2u(__hmul2(u2h(sc[2 * z]), u2h(up[z])));
+          sc[2 * z + 1] = h2u(__hmul2(u2h(sc[2 * z + 1]), u2h(up[z])));
+        }
+#pragma unroll
+        for (int q = 0; q < VCH; ++q) {
+          const int blk = q * VBPC + col_grp % VBPC;          // of this lane's columns
+          const float fq = __shfl_sync(0xffffffffu, fu[q * VBPC / 4], 8 * (blk & 3) + 4);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float both = f[nt][k & 1] * fq;
+#pragma unroll
+              for (int sp = 0; sp < CPU / 2; ++sp) o[nt][q * (CPU / 2) + sp][k] *= both;
+            }
+        }
       }
       uint32_t p[NT][2];
 #pragma unroll
@@ -404,84 +459,33 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
         p[nt][0] = transpose8(h2u(__floats2half2_rn(e[0], e[1])));
         p[nt][1] = transpose8(h2u(__floats2half2_rn(e[2], e[3])));
       }
-      // ---- values: (lo, step) of the row's blocks as columns, tokens as pairs ----
-      uint32_t sc[2 * SCH];
-      if constexpr (SCH == 2) {
-        uint32_t x[4];
-        ldsm4t(x, sta + vs_at);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sc[k] = x[k];
-      } else {
-        ldsm2t(sc[0], sc[1], sta + vs_at);
-      }
-      if (t0 + TOK > len) {                // what lies behind the sequence may be anything
-        const int t = t0 + 2 * c;
-        const uint32_t live0 = (t < len ? 0xffffu : 0u) | (t + 1 < len ? 0xffff0000u : 0u);
-        const uint32_t live1 = (t + 8 < len ? 0xffffu : 0u) | (t + 9 < len ? 0xffff0000u : 0u);
-#pragma unroll
-        for (int k = 0; k < 2 * SCH; ++k) sc[k] &= (k & 1) ? live1 : live0;
-      }
+      // ---- values ----
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
         mma16816(olo[nt], sc[0], SCH == 2 ? sc[2 * (SCH - 1)] : 0u, sc[1], SCH == 2 ? sc[2 * (SCH - 1) + 1] : 0u, p[nt][0], p[nt][1]);
-      auto add_codes = [&](const uint32_t (&sv)[2 * SCH]) {
 #pragma unroll
-        for (int q2 = 0; q2 < VCH; q2 += 2) {
-          uint32_t x[4];
-          if constexpr (VCH == 1) ldsm2t(x[0], x[1], sta + v_at);
-          else ldsm4t(x, (sta + v_at) ^ (q2 * 16u));
+      for (int q2 = 0; q2 < VCH; q2 += 2) {
+        uint32_t x[4];
+        if constexpr (VCH == 1) ldsm2t(x[0], x[1], sta + v_at);
+        else ldsm4t(x, (sta + v_at) ^ (q2 * 16u));
 #pragma unroll
-          for (int u = 0; u < (VCH == 1 ? 1 : 2); ++u) {
-            const int q = q2 + u, blk = q * VBPC + b_grp % VBPC, z = q * VBPC / 4, src = 8 * (blk & 3) + 4 + c;
-            const __half2 st0 = u2h(__shfl_sync(0xffffffffu, sv[2 * z], src));
-            const __half2 st1 = u2h(__shfl_sync(0xffffffffu, sv[2 * z + 1], src));
-            uint32_t ps[NT][2];
+        for (int u = 0; u < (VCH == 1 ? 1 : 2); ++u) {
+          const int q = q2 + u, blk = q * VBPC + b_grp % VBPC, z = q * VBPC / 4, src = 8 * (blk & 3) + 4 + c;
+          const __half2 st0 = u2h(__shfl_sync(0xffffffffu, sc[2 * z], src));
+          const __half2 st1 = u2h(__shfl_sync(0xffffffffu, sc[2 * z + 1], src));
+          uint32_t ps[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              ps[nt][0] = h2u(__hmul2(u2h(p[nt][0]), st0));
-              ps[nt][1] = h2u(__hmul2(u2h(p[nt][1]), st1));
-            }
-#pragma unroll
-            for (int sp = 0; sp < CPU / 2; ++sp) {
-              const uint32_t a0 = cc::codes_of<VB>(x[2 * u], 2 * sp), a1 = cc::codes_of<VB>(x[2 * u], 2 * sp + 1);
-              const uint32_t a2 = cc::codes_of<VB>(x[2 * u + 1], 2 * sp), a3 = cc::codes_of<VB>(x[2 * u + 1], 2 * sp + 1);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][q * (CPU / 2) + sp], a0, a1, a2, a3, ps[nt][0], ps[nt][1]);
-            }
-          }
-        }
-      };
-      __half2 top = u2h(sc[0]);
-#pragma unroll
-      for (int k = 1; k < 2 * SCH; ++k) top = __hmax2(top, u2h(sc[k]));
-      const bool big = (g & 1) && fmaxf(__low2float(top), __high2float(top)) >= cc::BIG_STEP;
-      if (!__any_sync(0xffffffffu, big)) {
-        add_codes(sc);
-      } else {
-        // steps of 32 and more apart from the others, smaller by 2^11, in sums that are too
-        uint32_t part[2 * SCH];
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-          const float f = pass ? cc::BIG_SCALE : 1.f;
-#pragma unroll
-          for (int k = 0; k < 2 * SCH; ++k) {
-            const float2 x = __half22float2(u2h(sc[k]));
-            const bool b0 = x.x >= cc::BIG_STEP, b1 = x.y >= cc::BIG_STEP;
-            part[k] = h2u(__floats2half2_rn(b0 == (pass == 1) ? x.x * f : 0.f, b1 == (pass == 1) ? x.y * f : 0.f));
+          for (int nt = 0; nt < NT; ++nt) {
+            ps[nt][0] = h2u(__hmul2(u2h(p[nt][0]), st0));
+            ps[nt][1] = h2u(__hmul2(u2h(p[nt][1]), st1));
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int sp = 0; sp < CPU / 2; ++sp) {
+            const uint32_t a0 = cc::codes_of<VB>(x[2 * u], 2 * sp), a1 = cc::codes_of<VB>(x[2 * u], 2 * sp + 1);
+            const uint32_t a2 = cc::codes_of<VB>(x[2 * u + 1], 2 * sp), a3 = cc::codes_of<VB>(x[2 * u + 1], 2 * sp + 1);
 #pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[nt][mt][k] *= f;
-          add_codes(part);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[nt][mt][k] *= 1.f / f;
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][q * (CPU / 2) + sp], a0, a1, a2, a3, ps[nt][0], ps[nt][1]);
+          }
         }
       }
     }
@@ -489,6 +493,10 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
     // ---- outputs to the merge buffer: of a feature, the columns of its block ----
     __syncthreads();
     const int own = g / VB;                  // block of unit g within its chunk
+    float back[VCH];                         // what takes 2^-24 and `up` of that block away again
+#pragma unroll
+    for (int q = 0; q < VCH; ++q)
+      back[q] = 0x1p24f / __low2float(u2h(__shfl_sync(0xffffffffu, up[q * VBPC / 4], 8 * ((q * VBPC + own) & 3) + 4)));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -511,8 +519,8 @@ __global__ void __launch_bounds__(cc::warps_of<NT, KB, VB>() * 32,
 #pragma unroll
             for (int sp = 0; sp < CPU / 2; ++sp) {
               const int mt = q * (CPU / 2) + sp, d = q * (128 / VB) + g * CPU + 2 * sp;
-              rec[d] = fmaf(o[nt][mt][k], 0x1p24f * cc::code_scale(VB, 2 * sp), lo);
-              rec[d + 1] = fmaf(o[nt][mt][2 + k], 0x1p24f * cc::code_scale(VB, 2 * sp + 1), lo);
+              rec[d] = fmaf(o[nt][mt][k], back[q] * cc::code_scale(VB, 2 * sp), lo);
+              rec[d + 1] = fmaf(o[nt][mt][2 + k], back[q] * cc::code_scale(VB, 2 * sp + 1), lo);
             }
           }
         }

@@ -299,7 +299,8 @@ typedef struct {
  * page_table[b][t / page_size].  All arrays are device memory and are read when the kernels run:
  * a captured graph replays with whatever they then hold.
  *   n_seqs    : sequences (0 is allowed: nothing is done)
- *   max_pages : row pitch of page_table (entries behind a sequence's last page are not read)
+ *   max_pages : row pitch of page_table (entries behind a sequence's last page are not read);
+ *               max_pages * page_size at most 2^30
  *   max_new   : the most rows of one sequence (an upper bound; jolt_cache_attend chooses its kernel by it)
  *   n_rows    : rows of the dense tensors; rows at or behind starts[n_seqs] are left as they were
  *   status_dev: one uint32 of device memory, OR-ed with what the kernels find (never cleared by

@@ -11,6 +11,8 @@ using namespace jolt;
 
 namespace {
 
+constexpr int MOST = 1 << 30;   // tokens of a sequence
+
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 jolt_status cache_args(const jolt_cache* c, const jolt_cache_batch* b, CacheArgs* ca, BatchArgs* ba) {
@@ -33,6 +35,9 @@ jolt_status cache_args(const jolt_cache* c, const jolt_cache_batch* b, CacheArgs
     return fail(JOLT_ERR_INVALID_ARG, "cache pools must be 16-byte aligned");
   if (b->n_seqs < 0 || b->max_pages < 0 || b->max_new < 0 || b->n_rows < 0)
     return fail(JOLT_ERR_INVALID_ARG, "negative batch size");
+  // a sequence's length rounded up to whole units of tokens stays an int
+  if ((long long)b->max_pages * c->page_size > MOST)
+    return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "%d pages of %d tokens hold more than 2^30", b->max_pages, c->page_size);
   if (b->n_seqs > 0 && (!b->page_table_dev || !b->lens_dev || !b->starts_dev || !b->status_dev))
     return fail(JOLT_ERR_INVALID_ARG, "null batch array");
   ca->codes[0] = (unsigned char*)c->k_codes_dev;

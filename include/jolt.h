@@ -298,11 +298,11 @@ typedef struct {
  * lens[b] - n_b + i of sequence b; position t is slot t % page_size of page
  * page_table[b][t / page_size].  All arrays are device memory and are read when the kernels run:
  * a captured graph replays with whatever they then hold.
- *   n_seqs    : sequences (0 is allowed: nothing is done)
+ *   n_seqs    : sequences, at most 2^30 (0 is allowed: nothing is done)
  *   max_pages : row pitch of page_table (entries behind a sequence's last page are not read);
  *               max_pages * page_size at most 2^30
  *   max_new   : the most rows of one sequence (an upper bound; jolt_cache_attend chooses its kernel by it)
- *   n_rows    : rows of the dense tensors; rows at or behind starts[n_seqs] are left as they were
+ *   n_rows    : rows of the dense tensors, at most 2^30; rows at or behind starts[n_seqs] are left as they were
  *   status_dev: one uint32 of device memory, OR-ed with what the kernels find (never cleared by
  *               them); jolt_cache_check reads it
  * A sequence with n_b < 0, n_b > max_new, rows outside [0, n_rows), lens[b] < n_b or

@@ -11,7 +11,7 @@ using namespace jolt;
 
 namespace {
 
-constexpr int MOST = 1 << 30;   // tokens of a sequence
+constexpr int MOST = 1 << 30;   // rows or sequences of a batch, tokens of a sequence
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -35,6 +35,9 @@ jolt_status cache_args(const jolt_cache* c, const jolt_cache_batch* b, CacheArgs
     return fail(JOLT_ERR_INVALID_ARG, "cache pools must be 16-byte aligned");
   if (b->n_seqs < 0 || b->max_pages < 0 || b->max_new < 0 || b->n_rows < 0)
     return fail(JOLT_ERR_INVALID_ARG, "negative batch size");
+  // a block's or a warp's first row, and the step behind the last sequence, stay ints
+  if (b->n_seqs > MOST || b->n_rows > MOST)
+    return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "a batch of %d sequences and %d rows; at most 2^30", b->n_seqs, b->n_rows);
   // a sequence's length rounded up to whole units of tokens stays an int
   if ((long long)b->max_pages * c->page_size > MOST)
     return fail(JOLT_ERR_UNSUPPORTED_SHAPE, "%d pages of %d tokens hold more than 2^30", b->max_pages, c->page_size);

@@ -446,6 +446,13 @@ class Attention:
         return self._run(layer, q, None, lse), lse
 
 
+def _int32(name, value):
+    """value for a 32-bit field, which would drop the bits above without a word"""
+    if value >> 31 not in (0, -1):
+        raise ValueError(f"{name} {value} does not fit in 32 bits")
+    return value
+
+
 _CACHE_DTYPES = {torch.bfloat16: JOLT_BF16, torch.float32: JOLT_F32, torch.float16: JOLT_F16}
 
 
@@ -468,9 +475,10 @@ class CacheBatch:
             raise ValueError("page_table [n_seqs, max_pages], lens [n_seqs] and starts [n_seqs + 1] are needed")
         if max_new < 0:
             raise ValueError("max_new must not be negative")
-        self.page_table, self.lens, self.starts, self.max_new = page_table, lens, starts, int(max_new)
+        self.page_table, self.lens, self.starts = page_table, lens, starts
+        self.max_new = _int32("max_new", int(max_new))
         self.device = page_table.device
-        self._c = CCacheBatch(lens.shape[0], page_table.shape[1], self.max_new, 0, page_table.data_ptr(),
+        self._c = CCacheBatch(_int32("n_seqs", lens.shape[0]), _int32("max_pages", page_table.shape[1]), self.max_new, 0, page_table.data_ptr(),
                               lens.data_ptr(), starts.data_ptr(), 0)
 
 
@@ -541,7 +549,7 @@ class QuantCache:
             if t is not None and t.device != device:
                 raise ValueError(f"everything must be on the cache's device {device}")
         b = CCacheBatch.from_buffer_copy(batch._c)
-        b.n_rows, b.status = rows, self._status_ptr
+        b.n_rows, b.status = _int32("rows", rows), self._status_ptr
         return self._layers[layer], b
 
     def _rows(self, t, name, heads):
@@ -603,7 +611,7 @@ class QuantCache:
         if q.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("q must be bf16 or fp16")
         c, b = self._call(layer, batch, rows, q, out)
-        o = CAttendOptions(scale, softcap, window)
+        o = CAttendOptions(scale, softcap, _int32("window", window))
         if slopes is not None or positions is not None or mask is not None or prefix is not None:
             self._extras(o, rows, nq, slopes, positions, mask, prefix)
         if out is None:

@@ -110,9 +110,7 @@ struct Scratch {
 };
 Scratch attend_scratch(const CacheArgs& c, const BatchArgs& a, int nq) {
   const long long rows = (long long)a.max_new * (nq / c.H);
-  // blocks of the kernel that takes this many rows (or more than it has), and rows of its pieces
-  const size_t blocks = rows > FEW_ROWS ? MANY_BLOCKS : 148 * (rows <= 16 ? 4 : 2);
-  const size_t tile = rows > 128 ? 256 : rows > FEW_ROWS ? 128 : rows <= 16 ? 16 : 32;
+  const size_t blocks = scratch_blocks(rows), tile = scratch_rows(rows);
   Scratch s;
   Bump m;
   s.notes = m.take(sizeof(int4) * blocks);

@@ -16,32 +16,35 @@ inline constexpr int FEW_ROWS = 32;
 
 inline constexpr int MANY_BLOCKS = 148;   // of the tensor-core kernel: one per SM
 
-// shared memory of the narrow kernel, and its blocks: as many as the GPU holds at once (by
-// registers 4, 3 or 2 per SM, by shared memory what 228 KB hold with 1 KB reserved for each)
-inline int few_smem(const CacheArgs& c, int nt) {
-  const int bk = c.bits[0], bv = c.bits[1];
-  if (c.D == 64)
-    return nt == 1 ? ca::Smem<64, 1>::bytes(bk, bv) : nt == 2 ? ca::Smem<64, 2>::bytes(bk, bv) : ca::Smem<64, 4>::bytes(bk, bv);
-  return nt == 1 ? ca::Smem<128, 1>::bytes(bk, bv) : nt == 2 ? ca::Smem<128, 2>::bytes(bk, bv) : ca::Smem<128, 4>::bytes(bk, bv);
+// What the scratch holds for calls with so many rows of a KV head: pieces of this many blocks, two of each, of this
+// many rows.  Every launch asserts that its blocks and pieces fit.
+inline constexpr int scratch_blocks(long long rows) { return rows > FEW_ROWS ? MANY_BLOCKS : 148 * (rows <= 16 ? 4 : 2); }
+inline constexpr int scratch_rows(long long rows) {
+  return rows > 128 ? 256 : rows > FEW_ROWS ? 128 : rows <= 16 ? 16 : 32;
 }
-inline int few_blocks(const CacheArgs& c, int nt) {
-  const int by_regs = nt == 1 ? 4 : nt == 2 ? 3 : 2, by_smem = 228 * 1024 / (few_smem(c, nt) + 1024);
-  return 148 * (by_regs < by_smem ? by_regs : by_smem);
+inline constexpr bool scratch_fits(int blocks, int piece_rows, long long rows) {
+  return blocks <= scratch_blocks(rows) && blocks * piece_rows <= scratch_blocks(rows) * scratch_rows(rows);
 }
 
 template <int D, int NT, int KB, int VB>
 jolt_status launch_codes(const CacheAttendArgs& A, cudaStream_t st) {
   using S = cc::Smem<D, NT, KB, VB>;
   constexpr int blocks = 148 * cc::blocks_per_sm<D, NT, KB, VB>();
+  static_assert(blocks <= JOIN_MOST && scratch_fits(blocks, S::ROWS, S::ROWS));
   CUDA_TRY(cudaFuncSetAttribute(cache_codes_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES));
   CUDA_TRY(launch_after(cache_codes_kernel<D, NT, KB, VB>, dim3(blocks), S::WARPS * 32, S::BYTES, st, A));
   CUDA_TRY(launch_after(cache_join_kernel<D, S::ROWS>, dim3(blocks, (unsigned)ceil_div(A.a.max_new * A.G, 512 / D)), 512, 0, st, A));
   return JOLT_OK;
 }
 
+// As many blocks as the GPU holds at once: by registers 4, 3 or 2 per SM, by shared memory what 228 KB hold with
+// 1 KB reserved for each.
 template <int D, int NT, int KB, int VB>
 jolt_status launch_few(const CacheAttendArgs& A, cudaStream_t st) {
-  const int smem = ca::Smem<D, NT>::bytes(KB, VB), blocks = few_blocks(A.c, NT);
+  constexpr int smem = ca::Smem<D, NT>::bytes(KB, VB);
+  constexpr int by_regs = NT == 1 ? 4 : NT == 2 ? 3 : 2, by_smem = 228 * 1024 / (smem + 1024);
+  constexpr int blocks = 148 * (by_regs < by_smem ? by_regs : by_smem);
+  static_assert(blocks <= JOIN_MOST && scratch_fits(blocks, 8 * NT, 8 * NT));
   CUDA_TRY(cudaFuncSetAttribute(cache_few_rows_kernel<D, NT, KB, VB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   CUDA_TRY(launch_after(cache_few_rows_kernel<D, NT, KB, VB>, dim3(blocks), ca::WARPS * 32, smem, st, A));
   CUDA_TRY(launch_after(cache_join_kernel<D, 8 * NT>, dim3(blocks, (unsigned)ceil_div(A.a.max_new * A.G, 512 / D)), 512, 0, st, A));
@@ -51,6 +54,7 @@ jolt_status launch_few(const CacheAttendArgs& A, cudaStream_t st) {
 template <int D, int KB, int VB, bool PAIR>
 jolt_status launch_many(const CacheAttendArgs& A, cudaStream_t st) {
   constexpr int smem = ct::Smem<D>::bytes(PAIR), rows = PAIR ? 256 : 128;
+  static_assert(scratch_fits(MANY_BLOCKS, rows, rows));
   CUDA_TRY(cudaFuncSetAttribute(cache_many_rows_kernel<D, KB, VB, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   CUDA_TRY(launch_after(cache_many_rows_kernel<D, KB, VB, PAIR>, dim3(MANY_BLOCKS), ct::THREADS, smem, st, A));
   CUDA_TRY(launch_after(cache_join_rows_kernel<D, rows>, dim3(MANY_BLOCKS, rows / 8), 256, 0, st, A));

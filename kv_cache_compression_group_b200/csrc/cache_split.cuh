@@ -153,12 +153,14 @@ __global__ void __launch_bounds__(256) cache_join_rows_kernel(CacheAttendArgs A)
   for (int i = 0; i < V; ++i) store_out(A, D, row0 + row / A.G, h * A.G + row % A.G, 32 * i + lane, o[i], l, m);
 }
 
-// Few rows of few jobs, which may have up to 74 pieces each: a CTA takes 512 / D rows, a thread one
-// feature; the pieces' maxima and sums first, then the weighted sums, eight loads under way.
+// Few rows of few jobs, which may have many pieces each (one of every block where there is one job): a CTA
+// takes 512 / D rows, a thread one feature; the pieces' maxima and sums first, then the weighted sums, eight
+// loads under way.
+constexpr int JOIN_MOST = 592;          // blocks of the launch whose pieces are joined
 template <int D, int ROWS>
 __global__ void __launch_bounds__(512) cache_join_kernel(CacheAttendArgs A) {
-  constexpr int REC = D + 4, MOST = 592, PER = 512 / D;
-  __shared__ float2 ml[PER][MOST];      // maximum and sum of every piece
+  constexpr int REC = D + 4, PER = 512 / D;
+  __shared__ float2 ml[PER][JOIN_MOST];   // maximum and sum of every piece
   cs::wait_for_predecessor();
   const int c0 = blockIdx.x, slot = threadIdx.x / D, d = threadIdx.x % D;
   const int4 note = A.notes[c0];

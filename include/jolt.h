@@ -364,8 +364,9 @@ typedef struct {
  *   out_dev : the same shape and type, its own strides
  *   scratch_dev: jolt_cache_attend_scratch_size bytes, 256-byte aligned, contents irrelevant; two
  *     calls (or replayed graphs) that may run at once need one each
- * Results do not depend on the other sequences of the batch beyond the order of fp32 sums, and are
- * the same in every run of the same call.  Asynchronous. */
+ * Results depend on the other sequences of the batch in roundings only (where a sequence's keys are split
+ * decides the order of fp32 sums and the maximum relative to which weights are rounded to fp16), and
+ * are the same in every run of the same call.  Asynchronous. */
 jolt_status jolt_cache_attend_scratch_size(const jolt_cache* cache, const jolt_cache_batch* batch, int32_t n_q_heads,
                                            size_t* bytes);
 jolt_status jolt_cache_attend(const jolt_cache* cache, const jolt_cache_batch* batch,

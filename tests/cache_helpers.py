@@ -77,6 +77,17 @@ class Paged:
         return torch.from_numpy(np.concatenate(x)).to(dtype)
 
 
+def refill(p, kv, rows):
+    """Store rows (one [len, H, D] array per sequence) as the keys (0) or values (1) of p."""
+    for s, x in enumerate(rows):
+        codes, scales, p.values[kv][s] = quantised(np.asarray(x, np.float64), p.bits[kv])
+        t = np.arange(p.lens[s])
+        at = p.table[s, t // p.page], slice(None), t % p.page
+        p.pools_np[2 * kv][at], p.pools_np[2 * kv + 1][at] = codes, scales
+    for i in (2 * kv, 2 * kv + 1):
+        p.pools[i][0].copy_(torch.from_numpy(p.pools_np[i]))
+
+
 def tree(rng, news, width):
     """(mask words, depths) of a random tree of drafted tokens for every sequence."""
     words = max(1, -(-max(news + [0]) // 32))

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from cache_helpers import Paged, quantised
+from cache_helpers import Paged, refill
 from kv_cache_compression_group_b200 import jolt as J
 
 pytestmark = pytest.mark.gpu
@@ -17,17 +17,6 @@ VALUE, LEAST = 2.0 ** -11, 2.0 ** -23
 # jobs of 128 and of 256 rows on the tensor cores
 ROWS = [1, 4, 7, 12, 24, 40, 160]
 SIZES = [1.0, 1e-2, 1e-3, 1e-4, 1e-5]
-
-
-def refill(p, kv, rows):
-    """Store rows (one [len, H, D] array per sequence) as the keys (0) or values (1) of p."""
-    for s, x in enumerate(rows):
-        codes, scales, p.values[kv][s] = quantised(np.asarray(x, np.float64), p.bits[kv])
-        for t in range(p.lens[s]):
-            at = p.table[s, t // p.page], slice(None), t % p.page
-            p.pools_np[2 * kv][at], p.pools_np[2 * kv + 1][at] = codes[t], scales[t]
-    for i in (2 * kv, 2 * kv + 1):
-        p.pools[i][0].copy_(torch.from_numpy(p.pools_np[i]))
 
 
 def fp16_out(want, tol):

@@ -420,7 +420,8 @@ void jolt_set_graphs(int32_t enable);
 /* Stage timing for measurement (no counterpart on the pages).  jolt_profile_begin starts
  * recording CUDA events around every internal stage launched by this thread (on the call's
  * stream); jolt_profile_end stops, SYNCHRONISES on the recorded events and writes one line
- * per stage, "name total_ms launches units\n", into buf (capacity cap, NUL-terminated).
+ * per stage, "name total_ms launches units\n", into buf (capacity cap, NUL-terminated).  Calls on a
+ * stream that is being captured are not timed.
  * Recording adds two event records per stage and changes no result. */
 jolt_status jolt_profile_begin(void);
 /* Number of kernels this library has launched in the process so far (its own kernels; work

@@ -66,7 +66,12 @@ struct ProfScope {
   ProfRec rec;
   cudaStream_t st;
   bool on;
-  ProfScope(const char* name, cudaStream_t s, long long units = 1) : st(s), on(g_prof.on) {
+  // (events captured into a graph cannot be read)
+  static bool capturing(cudaStream_t s) {
+    cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing(s, &c) != cudaSuccess || c != cudaStreamCaptureStatusNone;
+  }
+  ProfScope(const char* name, cudaStream_t s, long long units = 1) : st(s), on(g_prof.on && !capturing(s)) {
     if (!on) return;
     rec.name = name;
     rec.units = units;

@@ -285,6 +285,8 @@ struct Raw {
     else return (lane >> 3) % CH;
   }
 };
+// (Plain loads, not through the read-only path: the kernel may be brought up before the one that writes the rows has
+// ended, so they are not constant while it lives.)
 struct RawRegs {
   uint4 code[4];
   uint32_t scale[4];
@@ -306,15 +308,15 @@ __device__ __forceinline__ void raw_load_rows(RawRegs& r, const unsigned char* c
       for (int k = 0; k < W::BLKS; ++k) r.scale[i * W::BLKS + k] = 0u;
       continue;
     }
-    r.code[i] = __ldg(src);
+    r.code[i] = *src;
     if constexpr (W::BLKS == 1) {
-      r.scale[i] = __ldg(sc);
+      r.scale[i] = *sc;
     } else if constexpr (W::BLKS == 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(sc));
+      const uint2 v = *reinterpret_cast<const uint2*>(sc);
       r.scale[2 * i] = v.x;
       r.scale[2 * i + 1] = v.y;
     } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(sc));
+      const uint4 v = *reinterpret_cast<const uint4*>(sc);
       r.scale[0] = v.x;
       r.scale[1] = v.y;
       r.scale[2] = v.z;

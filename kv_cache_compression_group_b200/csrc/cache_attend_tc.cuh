@@ -170,8 +170,10 @@ __device__ __forceinline__ bool elect_one() {
   return ok != 0;
 }
 // Registers of a thread of each role.  640 threads are launched with 96, 61440 in all, which the shares
-// 256 x 120 + 256 x 88 + 128 x 64 use up.
-constexpr int SOFTMAX_REGS = 120, DEQUANT_REGS = 88, ISSUE_REGS = 64;
+// 256 x 120 + 256 x 88 + 128 x 64 use up.  (With fewer at the launch the softmax warps would wait for theirs
+// forever: launch_many refuses a kernel that was compiled otherwise.)
+constexpr int LAUNCH_REGS = 96, SOFTMAX_REGS = 120, DEQUANT_REGS = 88, ISSUE_REGS = 64;
+static_assert(256 * SOFTMAX_REGS + 256 * DEQUANT_REGS + 128 * ISSUE_REGS <= THREADS * LAUNCH_REGS);
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));

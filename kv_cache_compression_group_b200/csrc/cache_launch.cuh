@@ -55,6 +55,11 @@ template <int D, int KB, int VB, bool PAIR>
 jolt_status launch_many(const CacheAttendArgs& A, cudaStream_t st) {
   constexpr int smem = ct::Smem<D>::bytes(PAIR), rows = PAIR ? 256 : 128;
   static_assert(scratch_fits(MANY_BLOCKS, rows, rows));
+  static const int regs = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, cache_many_rows_kernel<D, KB, VB, PAIR>) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs < ct::LAUNCH_REGS) return fail(JOLT_ERR_CUDA, "the kernel has %d registers at its launch, needs %d", regs, ct::LAUNCH_REGS);
   CUDA_TRY(cudaFuncSetAttribute(cache_many_rows_kernel<D, KB, VB, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   CUDA_TRY(launch_after(cache_many_rows_kernel<D, KB, VB, PAIR>, dim3(MANY_BLOCKS), ct::THREADS, smem, st, A));
   CUDA_TRY(launch_after(cache_join_rows_kernel<D, rows>, dim3(MANY_BLOCKS, rows / 8), 256, 0, st, A));

@@ -247,7 +247,8 @@ jolt_status jolt_attend(const void* blob_dev, const void* ws_dev, size_t ws_byte
 
 /* jolt_attend that also gives the softmax's log-sum-exp, lse_dev [n_q_heads] fp32 (natural
  * logarithm of sum_t exp(s_t)): with it, attention over further keys can be joined to the
- * output (the prefix of jolt_cache_attend).  Same arguments and outputs otherwise. */
+ * output (the prefix of jolt_cache_attend).  Same arguments and outputs otherwise; like jolt_attend it
+ * synchronises, so it cannot be captured into a graph (jolt_cache_attend can). */
 jolt_status jolt_attend_state(const void* blob_dev, const void* ws_dev, size_t ws_bytes, int32_t layer,
                               const float* q_dev, int32_t n_q_heads, float* out_dev, float* lse_dev,
                               void* scratch_dev, size_t scratch_bytes, void* stream);
@@ -278,7 +279,8 @@ jolt_status jolt_quant_baseline(const jolt_shape* shape, const void* k_dev, cons
  * the codes: [n_pages][n_heads][page_size][head_dim * bits / 8] bytes, the codes of a row as one
  * little-endian bit string (2 * bits bytes per block); of the scales:
  * [n_pages][n_heads][page_size][head_dim / 16] fp16 pairs (lo, step).  Pointers 16-byte aligned.
- *   head_dim 64 or 128; page_size a power of two in [16, 4096]; bits 2, 4 or 8;
+ *   head_dim 64 or 128 (prompts compressed at 16 or 32 cannot be joined to it); page_size a power of
+ *   two in [16, 4096]; bits 2, 4 or 8;
  *   n_pages * page_size * n_heads below 2^31 (the bytes may pass 2^32). */
 typedef struct {
   int32_t n_heads;
@@ -341,7 +343,7 @@ typedef struct {
   float scale;          /* of q . k; 0 = 1 / sqrt(head_dim) */
   float softcap;        /* c > 0: s = c tanh(s / c), before the bias, c in [1e-6, 1e30]; 0 = none */
   int32_t window;       /* w > 0: a row at position p sees keys at positions above p - w only; 0 = all */
-  int32_t mask_words;   /* 32-bit words per row of `mask`, at least max_new / 32 */
+  int32_t mask_words;   /* 32-bit words per row of `mask`, at least max_new / 32, rounded up */
   const float* slopes_dev;       /* [n_q_heads]: s -= slope * (p_query - p_key); NULL = no bias */
   const int32_t* positions_dev;  /* [n_rows] positions of the new rows, as queries and as keys; NULL =
                                     their place in the sequence.  Below lens[b] - n_b is not allowed */

@@ -19,9 +19,12 @@
 //     S = Q K^T, of the one group while the other is at its softmax.  (Scores in two halves of 64
 //     keys, to overlap a group's products with its own softmax, were slower: a product with N = 64
 //     waits for the shared memory that Q is read from again, and there are twice the commits.)
-// What bounds it at D = 128: the two products take 1024 cycles per 128 x 128 tile, its 16384
-// exponentials 1024 at 16 per cycle, and the instructions of softmax (about 450 per scheduler) and
-// of dequantisation (about 600, once per 256 rows) come next to them.
+// What bounds it at D = 128: 2048 new rows of 32 query heads over 16384 tokens (8 KV heads, 4 bits) take 650 us,
+// 5800 clocks for a tile of 256 rows and 128 tokens.  Its products take 2048 of them (tensor pipe 37 %), its
+// exponentials 2048 at 16 per clock (that unit 38 %), instructions issue in 43 %: no unit is full, the rest is
+// the roles' waiting for one another.  With 128 rows (wide trees, 124 us for 16 sequences of up to 8192 tokens)
+// tensor pipe and exponentials are at 22 %, issue at 39 %.  The compiler holds every role to the launch's 96
+// registers and spills: 466 to 502 bytes of stores and 592 to 804 of loads, by instance.
 //
 // Every wait is bounded; after one gave up, the roles keep their barrier schedule without waiting or
 // issuing, so the CTA ends, and the issued products are drained before tensor memory is freed.

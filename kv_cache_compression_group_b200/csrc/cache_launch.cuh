@@ -10,8 +10,12 @@
 
 namespace jolt {
 
-// Rows of one KV head that the narrow kernels take.  (32 rows over 4 sequences of up to 16384 tokens, D = 64,
-// 8 bits: 60 us there and 123 us in the tensor-core kernel, whose tiles have 128 rows.)
+// Rows of one KV head that the narrow kernels take.  32 rows of 8 KV heads there and in the tensor-core kernel,
+// whose tiles have 128 rows, in us, at 2, 4 and 8 bits:
+//   16 sequences of 8192 tokens:  D = 64: 80, 84, 88 and 119, 109, 112;  D = 128: 121, 127, 131 and 131, 135, 152
+//   one of 65536 tokens:          D = 64: 49, 49, 52 and 70, 64, 68;     D = 128: 66, 71, 74 and 80, 91, 96
+//   one of 2000 tokens:           D = 64: 22.7 and 20.7;                 D = 128: 27 and 27
+// With 17 rows the narrow ones take 5 to 10 % less, the other as long.
 inline constexpr int FEW_ROWS = 32;
 
 inline constexpr int MANY_BLOCKS = 148;   // of the tensor-core kernel: one per SM

@@ -595,7 +595,8 @@ class QuantCache:
     def attend(self, layer: int, q: torch.Tensor, batch: CacheBatch, scale: float = 0.0, softcap: float = 0.0,
                window: int = 0, slopes=None, positions=None, mask=None, prefix=None, out=None, stream=None):
         """Attention of rows q [rows, n_q_heads, head_dim] (bf16 or fp16), whose keys and values are
-        written already, over their sequences; returns the output, in q's type.
+        written already, over their sequences; returns the output, in q's type (out, if given; rows that
+        belong to no sequence are left as they are).
 
         scale: of q . k, 0 for 1 / sqrt(head_dim).  softcap c > 0: scores c tanh(s / c).
         window w > 0: positions above p - w only.  slopes [n_q_heads] fp32: scores minus

@@ -185,7 +185,7 @@ def _on_its_stream(f):
         device = (args[0] if args else kw[names[0]]).device
         index = device.index                            # None: the current device's, or not on a GPU (f refuses it)
         if stream is None:
-            if index is None or index == torch.cuda.current_device():
+            if index is None or index == torch._C._cuda_getDevice():
                 return f(*args, **kw)
             with torch.cuda.device(device):
                 return f(*args, **kw)
@@ -549,7 +549,7 @@ class QuantCache:
             if t is not None and t.device != device:
                 raise ValueError(f"everything must be on the cache's device {device}")
         b = CCacheBatch.from_buffer_copy(batch._c)
-        b.n_rows, b.status = _int32("rows", rows), self._status_ptr
+        b.n_rows, b.status = rows if rows < 1 << 31 else _int32("rows", rows), self._status_ptr
         return self._layers[layer], b
 
     def _rows(self, t, name, heads):
@@ -612,7 +612,7 @@ class QuantCache:
         if q.dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("q must be bf16 or fp16")
         c, b = self._call(layer, batch, rows, q, out)
-        o = CAttendOptions(scale, softcap, _int32("window", window))
+        o = CAttendOptions(scale, softcap, window if window < 1 << 31 else _int32("window", window))
         if slopes is not None or positions is not None or mask is not None or prefix is not None:
             self._extras(o, rows, nq, slopes, positions, mask, prefix)
         if out is None:

@@ -19,6 +19,7 @@ def notes(monkeypatch):
         yield
         log.append("back")
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
     monkeypatch.setattr(torch.cuda, "device", switch)
     monkeypatch.setattr(torch.cuda, "stream", switch)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: ("current", device))

@@ -562,6 +562,14 @@ class QuantCache:
             raise ValueError(f"the features of {name} must be contiguous")
         return row, head
 
+    def _out_rows(self, t, name, heads):
+        """As _rows, of rows that are written: no two of them in one place."""
+        row, head = self._rows(t, name, heads)
+        (small, n), (large, m) = sorted(((row, t.shape[0]), (head, heads)))
+        if t.shape[0] and (n > 1 and small < self.head_dim or m > 1 and large < (n - 1) * small + self.head_dim):
+            raise ValueError(f"the rows and heads of {name} must not overlap")
+        return row, head
+
     @_on_its_stream
     def write(self, layer: int, k: torch.Tensor, v: torch.Tensor, batch: CacheBatch, stream=None):
         """Quantise rows k, v [rows, n_heads, head_dim] (bf16, fp16 or fp32, strided rows and heads)
@@ -583,10 +591,12 @@ class QuantCache:
             shape = (int(rows), self.n_heads, self.head_dim)
             out = tuple(torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
         k, v = out
-        ks = self._rows(k, "out[0]", self.n_heads)
-        vs = self._rows(v, "out[1]", self.n_heads)
+        ks = self._out_rows(k, "out[0]", self.n_heads)
+        vs = self._out_rows(v, "out[1]", self.n_heads)
         if k.dtype != dtype or v.dtype != dtype or k.shape != v.shape or k.shape[0] != rows:
             raise ValueError("out must be two tensors of dtype and rows")
+        if k.data_ptr() == v.data_ptr() and k.numel():
+            raise ValueError("the outputs of k and v must not overlap")
         c, b = self._call(layer, batch, k.shape[0], k, v)
         self._run(lib().jolt_cache_read, c, b, _CACHE_DTYPES[dtype], k.data_ptr(), v.data_ptr(), *ks, *vs)
         return k, v
@@ -617,14 +627,17 @@ class QuantCache:
             self._extras(o, rows, nq, slopes, positions, mask, prefix)
         if out is None:
             out = torch.empty((rows, nq, self.head_dim), dtype=q.dtype, device=self.device)
+            out_strides = nq * self.head_dim, self.head_dim
         elif out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("out must have q's shape and type")
+        else:
+            out_strides = self._out_rows(out, "out", nq)
         # a scratch of its own for every call, from the pool of the stream that it runs on: a later call
         # can only get it behind this one, and two captured graphs with pools of their own never share one
         nbytes = self._scratch_bytes(c, b, nq)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         self._run(lib().jolt_cache_attend, c, b, o, q.data_ptr(), _CACHE_DTYPES[q.dtype], nq, *qs,
-                  out.data_ptr(), *self._rows(out, "out", nq), scratch.data_ptr(), nbytes)
+                  out.data_ptr(), *out_strides, scratch.data_ptr(), nbytes)
         return out
 
     def _extras(self, o, rows, nq, slopes, positions, mask, prefix):
